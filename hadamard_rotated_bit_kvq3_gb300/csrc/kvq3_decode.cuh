@@ -393,7 +393,7 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
   return v;
 }
 
-// N bytes (1..32, a power of two) at shared address a + OFF as 32-bit words.
+// N bytes (1..64, a power of two) at shared address a + OFF as 32-bit words.
 template <int N, int OFF>
 __device__ __forceinline__ void lds_bytes(uint32_t a, uint32_t (&w)[(N + 3) / 4]) {
   if constexpr (N == 1) w[0] = lds8<OFF>(a);
@@ -406,9 +406,14 @@ __device__ __forceinline__ void lds_bytes(uint32_t a, uint32_t (&w)[(N + 3) / 4]
     const uint4 v = lds128<OFF>(a);
     w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
   } else {
-    const uint4 v = lds128<OFF>(a), u = lds128<OFF + 16>(a);
-    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-    w[4] = u.x; w[5] = u.y; w[6] = u.z; w[7] = u.w;
+    static_assert(N == 32 || N == 64, "scale bytes of one or two tokens");
+#pragma unroll
+    for (int h = 0; h < N / 32; ++h) {
+      const uint4 v = h == 0 ? lds128<OFF>(a) : lds128<OFF + 32>(a);
+      const uint4 u = h == 0 ? lds128<OFF + 16>(a) : lds128<OFF + 48>(a);
+      w[8 * h + 0] = v.x; w[8 * h + 1] = v.y; w[8 * h + 2] = v.z; w[8 * h + 3] = v.w;
+      w[8 * h + 4] = u.x; w[8 * h + 5] = u.y; w[8 * h + 6] = u.z; w[8 * h + 7] = u.w;
+    }
   }
 }
 
