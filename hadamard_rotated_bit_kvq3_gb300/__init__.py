@@ -20,6 +20,8 @@ __all__ = [
     "kvq3_cache_sizes", "kvq3_rotate", "kvq3_write", "kvq3_write_chunk", "kvq3_decode_workspace_size",
     "kvq3_decode_attn", "kvq3_decode_attn_noalloc", "kvq3_prefill_workspace_size", "kvq3_prefill_attn",
     "kvq3_dequant_debug", "kvq3_calib_sse", "kvq3_calibrate_workspace_size", "kvq3_calibrate_so4", "Rotation",
+    "kvq3_key_bounds", "kvq3_page_scores", "kvq3_page_select", "kvq3_decode_pages_workspace_size",
+    "kvq3_decode_attn_pages", "kvq3_remap_workspace_size", "kvq3_remap", "kvq3_compact",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -33,7 +35,7 @@ KVQ3_ROT_SO4 = 2
 KVQ3_ROT_SO4_PAIR = 4
 SCALE_TYPES = {"f32": 0, "f16": 1, "e4m3": 2, "e4m3zp": 3}
 DEV_BITS = {"bad_seq": 1, "bad_pos": 2, "bad_page": 4, "bad_len": 8, "bad_code": 16, "timeout": 32,
-            "check": 64}
+            "check": 64, "no_page": 128}
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(
@@ -87,6 +89,14 @@ _SIGS = {
                                                _p]),
     "kvq3_calibrate_workspace_size": (ctypes.c_int, [_D, _i32, ctypes.POINTER(_sz)]),
     "kvq3_calibrate_so4": (ctypes.c_int, [_p, _D, _p, _i64, _i32, _i32, _f32, _u64, _p, _sz, _p, _p, _p]),
+    "kvq3_key_bounds": (ctypes.c_int, [_D, _C, _p, _p, _p, _p]),
+    "kvq3_page_scores": (ctypes.c_int, [_p, _D, _C, _p, _p, _i32, _p, _p, _p]),
+    "kvq3_page_select": (ctypes.c_int, [_D, _C, _p, _i32, _i32, _i32, _p, _p, _p, _p]),
+    "kvq3_decode_pages_workspace_size": (ctypes.c_int, [_D, _i32, _i32, ctypes.POINTER(_sz)]),
+    "kvq3_decode_attn_pages": (ctypes.c_int, [_p, _D, _C, _p, _i32, _f32, _p, _p, _i32, _p, _p, _sz, _p, _p]),
+    "kvq3_remap_workspace_size": (ctypes.c_int, [_D, ctypes.POINTER(_sz)]),
+    "kvq3_remap": (ctypes.c_int, [_D, _C, _p, _p, _p, _p, _p, _sz, _p, _p]),
+    "kvq3_compact": (ctypes.c_int, [_D, _C, _p, _p, _i32, _p, _p, _i32, _p, _p]),
 }
 for _name, (_res, _args) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -323,6 +333,121 @@ def kvq3_dequant_debug(h, desc: CacheDesc, cache: Cache, seq: int, kv_head: int,
     _check(lib.kvq3_dequant_debug(h, ctypes.byref(desc), ctypes.byref(cache), seq, kv_head, which,
                                   t0, nt, _ptr(out), _ptr(codes_out), _ptr(dev_status),
                                   _stream(stream)), "kvq3_dequant_debug")
+
+
+# ---- page operators (sparse decode, page management).  These calls take
+# several tensors whose shapes must agree with the cache description, so the
+# binding checks them: a tensor of another type, shape, layout or device is a
+# ValueError before anything is launched.
+def _need(t, name: str, dtype, shape, where: str) -> None:
+    import torch
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor of type {dtype} and shape {shape}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{where}: {name} is on {t.device}, the call runs on the current device "
+                         f"{torch.cuda.current_device()}")
+
+
+def kvq3_key_bounds(desc: CacheDesc, cache: Cache, first_pos, bounds, dev_status=None, stream=None) -> None:
+    """bounds: fp16 [num_pages or more][Hkv][2][d]: minimum and maximum of the
+    rotated keys of every page that holds a position from first_pos (int32 [B],
+    None: 0) on; the others are left as they were."""
+    import torch
+    w = "kvq3_key_bounds"
+    if first_pos is not None:
+        _need(first_pos, "first_pos", torch.int32, (desc.batch,), w)
+    _need(bounds, "bounds", torch.float16, (max(desc.num_pages, bounds.shape[0]), desc.num_kv_heads, 2, desc.head_dim), w)
+    _check(lib.kvq3_key_bounds(ctypes.byref(desc), ctypes.byref(cache), _ptr(first_pos), _ptr(bounds),
+                               _ptr(dev_status), _stream(stream)), w)
+
+
+def kvq3_page_scores(h, desc: CacheDesc, cache: Cache, bounds, q, scores, dev_status=None, stream=None) -> None:
+    """scores: fp32 [B][Hkv][max_pages_per_seq] of the queries q, fp16
+    [B][Hq][d], against each page's bounds, fp16 [num_pages or more][Hkv][2][d]."""
+    import torch
+    w = "kvq3_page_scores"
+    _need(bounds, "bounds", torch.float16, (max(desc.num_pages, bounds.shape[0]), desc.num_kv_heads, 2, desc.head_dim), w)
+    _need(q, "q", torch.float16, (desc.batch, q.shape[1], desc.head_dim), w)
+    _need(scores, "scores", torch.float32, (desc.batch, desc.num_kv_heads, desc.max_pages_per_seq), w)
+    _check(lib.kvq3_page_scores(h, ctypes.byref(desc), ctypes.byref(cache), _ptr(bounds), _ptr(q), int(q.shape[1]),
+                                _ptr(scores), _ptr(dev_status), _stream(stream)), w)
+
+
+def kvq3_page_select(desc: CacheDesc, cache: Cache, scores, budget: int, sinks: int, recent: int, pages, counts,
+                     dev_status=None, stream=None) -> None:
+    """pages: int32 [B][Hkv][budget], ascending, then -1; counts: int32
+    [B][Hkv]; scores: fp32 [B][Hkv][max_pages_per_seq]."""
+    import torch
+    w = "kvq3_page_select"
+    heads = (desc.batch, desc.num_kv_heads)
+    _need(scores, "scores", torch.float32, (*heads, desc.max_pages_per_seq), w)
+    _need(pages, "pages", torch.int32, (*heads, budget), w)
+    _need(counts, "counts", torch.int32, heads, w)
+    _check(lib.kvq3_page_select(ctypes.byref(desc), ctypes.byref(cache), _ptr(scores), budget, sinks, recent,
+                                _ptr(pages), _ptr(counts), _ptr(dev_status), _stream(stream)), w)
+
+
+def kvq3_decode_pages_workspace_size(desc: CacheDesc, num_q_heads: int, max_selected: int) -> int:
+    n = _sz()
+    _check(lib.kvq3_decode_pages_workspace_size(ctypes.byref(desc), num_q_heads, max_selected, ctypes.byref(n)),
+           "kvq3_decode_pages_workspace_size")
+    return n.value
+
+
+def kvq3_decode_attn_pages(h, desc: CacheDesc, cache: Cache, q, pages, counts, out, workspace, sm_scale: float = 0.0,
+                           dev_status=None, stream=None) -> None:
+    """q, out: fp16 [B][Hq][d]; pages: int32 [B][Hkv][n], strictly ascending;
+    counts: int32 [B][Hkv]; workspace: uint8 CUDA tensor
+    (kvq3_decode_pages_workspace_size(desc, Hq, n) bytes)."""
+    import torch
+    w = "kvq3_decode_attn_pages"
+    heads = (desc.batch, desc.num_kv_heads)
+    _need(q, "q", torch.float16, (desc.batch, q.shape[1], desc.head_dim), w)
+    _need(out, "out", torch.float16, tuple(q.shape), w)
+    _need(pages, "pages", torch.int32, (*heads, pages.shape[2]), w)
+    _need(counts, "counts", torch.int32, heads, w)
+    _check(lib.kvq3_decode_attn_pages(h, ctypes.byref(desc), ctypes.byref(cache), _ptr(q), int(q.shape[1]),
+                                      float(sm_scale), _ptr(pages), _ptr(counts), int(pages.shape[2]), _ptr(out),
+                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                      _ptr(dev_status), _stream(stream)), w)
+
+
+def kvq3_remap_workspace_size(desc: CacheDesc) -> int:
+    n = _sz()
+    _check(lib.kvq3_remap_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "kvq3_remap_workspace_size")
+    return n.value
+
+
+def kvq3_remap(desc: CacheDesc, cache: Cache, src, new_lens, table_out, lens_out, workspace, dev_status=None,
+               stream=None) -> None:
+    """src, new_lens, lens_out: int32 [B]; table_out: int32 [B][max_pages_per_seq],
+    not the cache's table; workspace: uint8 CUDA tensor
+    (kvq3_remap_workspace_size bytes)."""
+    import torch
+    w = "kvq3_remap"
+    rows = (desc.batch,)
+    _need(src, "src", torch.int32, rows, w)
+    _need(new_lens, "new_lens", torch.int32, rows, w)
+    _need(lens_out, "lens_out", torch.int32, rows, w)
+    _need(table_out, "table_out", torch.int32, (desc.batch, desc.max_pages_per_seq), w)
+    _check(lib.kvq3_remap(ctypes.byref(desc), ctypes.byref(cache), _ptr(src), _ptr(new_lens), _ptr(table_out),
+                          _ptr(lens_out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                          _ptr(dev_status), _stream(stream)), w)
+
+
+def kvq3_compact(desc: CacheDesc, cache: Cache, src_seq, dst_seq, keep, n_keep, dev_status=None, stream=None) -> None:
+    """src_seq, dst_seq, n_keep: int32 [n]; keep: int32 [n][Hkv][k], positions
+    of the source that become positions 0, 1, ... of the destination."""
+    import torch
+    w = "kvq3_compact"
+    rows = (src_seq.shape[0],)
+    _need(src_seq, "src_seq", torch.int32, rows, w)
+    _need(dst_seq, "dst_seq", torch.int32, rows, w)
+    _need(n_keep, "n_keep", torch.int32, rows, w)
+    _need(keep, "keep", torch.int32, (*rows, desc.num_kv_heads, keep.shape[-1]), w)
+    _check(lib.kvq3_compact(ctypes.byref(desc), ctypes.byref(cache), _ptr(src_seq), _ptr(dst_seq), rows[0],
+                            _ptr(keep), _ptr(n_keep), int(keep.shape[-1]), _ptr(dev_status), _stream(stream)), w)
 
 
 class Rotation:

@@ -282,6 +282,150 @@ kvq3_status kvq3_test_prefill_attn_polls(kvq3_rotation rot, const kvq3_cache_des
 
 }  // extern "C"
 
+// ------------------------------------------------------------------ selected pages
+// Attention over selected pages runs the decode kernel on another view of the
+// same pool: a record pair (K and V of one page and kv head) is a page of its
+// own, number page * Hkv + kv head, and every (sequence, kv head) a sequence
+// of one kv head whose page table is its list.  The list is ascending, so only
+// its last page can be part filled, and the view's length says how far.
+namespace {
+
+constexpr int kListThreads = 256;
+
+// The view's page table [units][row] and lengths [units].
+__global__ void __launch_bounds__(kListThreads)
+    page_list_kernel(const __grid_constant__ CacheGeom g, const int32_t* __restrict__ page_table,
+                     const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ pages,
+                     const int32_t* __restrict__ counts, int32_t row, int32_t* __restrict__ vtable,
+                     int32_t* __restrict__ vlens, int32_t* status) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t units = (int64_t)g.batch * g.hkv, total = units * row;
+  const int64_t cap = (int64_t)g.max_pages * g.page_size;
+  for (int64_t k = (int64_t)blockIdx.x * kListThreads + threadIdx.x; k < total; k += (int64_t)gridDim.x * kListThreads) {
+    const int64_t u = k / row;
+    const int i = (int)(k - u * row);
+    const int b = (int)(u / g.hkv), kvh = (int)(u - (int64_t)b * g.hkv);
+    const int64_t len = seq_lens[b];
+    int c = counts[u];
+    if (len < 0 || len > cap || c < 0 || c > row) {
+      if (i == 0) set_status(status, KVQ3_DEV_BAD_LEN);
+      c = 0;
+    }
+    int64_t page = -1;
+    bool part = false;
+    if (i < c) {
+      const int64_t lp = pages[k];
+      // a page of the sequence, above the entry before it; a part-filled page can only be the last one
+      if (lp >= 0 && lp * g.page_size < len && (i == 0 || lp > pages[k - 1])) {
+        part = (lp + 1) * g.page_size > len;
+        if (!part || i == c - 1) page = page_of(g, page_table, b, lp);
+      }
+      if (page < 0) set_status(status, KVQ3_DEV_BAD_PAGE);
+    }
+    vtable[k] = page < 0 ? -1 : (int32_t)(page * g.hkv + kvh);
+    // tokens of the view: every listed page whole, but the last one up to the length
+    if (c == 0 ? i == 0 : i == c - 1)
+      vlens[u] = c == 0 ? 0 : (int32_t)((int64_t)c * g.page_size - (part && page >= 0 ? g.page_size - len % g.page_size : 0));
+  }
+}
+
+// The view's geometry; KVQ3_ERR_UNSUPPORTED where an index would pass 31 bits.
+kvq3_status pages_view(const CacheGeom& g, int32_t hq, int32_t row, CacheGeom* v) {
+  kvq3_status s = check_heads(g, hq);
+  if (s != KVQ3_OK) return s;
+  if (row < 1) return KVQ3_ERR_INVALID_ARG;
+  const int64_t lim = (int64_t)1 << 31;
+  if (g.num_pages >= lim / g.hkv || (int64_t)g.batch * hq >= lim || (int64_t)row * g.page_size >= lim)
+    return KVQ3_ERR_UNSUPPORTED;
+  *v = g;
+  v->hkv = 1;
+  v->batch = g.batch * g.hkv;
+  v->max_pages = row;
+  v->num_pages = g.num_pages * g.hkv;
+  v->page_bytes = 2 * g.record_bytes;
+  return KVQ3_OK;
+}
+
+// Bytes of the view's table and lengths ahead of the decode workspace.
+size_t view_bytes(const CacheGeom& v) { return ((size_t)v.batch * ((size_t)v.max_pages + 1) * 4 + 255) / 256 * 256; }
+
+}  // namespace
+
+extern "C" {
+
+kvq3_status kvq3_decode_pages_workspace_size(const kvq3_cache_desc* desc, int32_t num_q_heads, int32_t max_selected,
+                                             size_t* bytes) {
+  CacheGeom g, v;
+  kvq3_status s = make_geom(desc, &g);
+  if (s != KVQ3_OK) return s;
+  if (!bytes) return KVQ3_ERR_INVALID_ARG;
+  if ((s = pages_view(g, num_q_heads, max_selected, &v)) != KVQ3_OK) return s;
+  DecodePlan plan;
+  if ((s = plan_for(v, num_q_heads / g.hkv, &plan)) != KVQ3_OK) return s;
+  *bytes = view_bytes(v) + plan.ws_bytes;
+  return KVQ3_OK;
+}
+
+kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc* desc, const kvq3_cache* cache,
+                                   const void* q, int32_t num_q_heads, float sm_scale, const int32_t* pages,
+                                   const int32_t* counts, int32_t max_selected, void* out, void* workspace,
+                                   size_t ws_bytes, int32_t* dev_status, void* stream) {
+  CacheGeom g, v;
+  kvq3_status s = make_geom(desc, &g);
+  if (s != KVQ3_OK) return s;
+  if (!rot || rot->d != g.d || !q || !out || !pages || !counts) return KVQ3_ERR_INVALID_ARG;
+  if ((s = check_cache(g, cache, true)) != KVQ3_OK) return s;
+  if ((s = pages_view(g, num_q_heads, max_selected, &v)) != KVQ3_OK) return s;
+  if (!(sm_scale <= 0.0f || isfinite(sm_scale))) return KVQ3_ERR_INVALID_ARG;
+  const int G = num_q_heads / g.hkv;
+  DecodePlan plan;
+  if ((s = plan_for(v, G, &plan)) != KVQ3_OK) return s;
+  const size_t head = view_bytes(v);
+  if (!workspace || ws_bytes < head + plan.ws_bytes || reinterpret_cast<uintptr_t>(workspace) % 256)
+    return KVQ3_ERR_WORKSPACE;
+  int32_t* vtable = static_cast<int32_t*>(workspace);
+  int32_t* vlens = vtable + (size_t)v.batch * v.max_pages;
+  char* ws = static_cast<char*>(workspace) + head;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t blocks = ((int64_t)v.batch * v.max_pages + kListThreads - 1) / kListThreads;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(blocks, (int64_t)sm_count() * 8));
+  cfg.blockDim = dim3(kListThreads);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, page_list_kernel, g, cache->page_table, cache->seq_lens, pages, counts, max_selected,
+                         vtable, vlens, dev_status) != cudaSuccess)
+    return KVQ3_ERR_CUDA;
+
+  DecodeParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.g = v;
+  prm.pool = static_cast<const uint8_t*>(cache->pool);
+  prm.page_table = vtable;
+  prm.seq_lens = vlens;
+  prm.q = static_cast<const __half*>(q);
+  prm.ws = reinterpret_cast<float*>(ws);
+  prm.unit_cta = reinterpret_cast<int32_t*>(ws + ((size_t)plan.ctas + (size_t)v.batch) * G * (g.d + 2) * sizeof(float));
+  prm.status = dev_status;
+  prm.G = G;
+  prm.Hq = G;
+  const double sc = sm_scale > 0.0f ? (double)sm_scale : 1.0 / sqrt((double)g.d);
+  prm.qk_scale = (float)(sc * 1.4426950408889634);  // log2(e): softmax in base 2
+  prm.inv_sqrt_d = inv_sqrt(g.d);
+  prm.slot_floats = (uint32_t)(G * (g.d + 2));
+  prm.wait_limit = kWaitPolls;
+  prm.out_half = 1;
+  return run_for(v, plan, prm, rot->params, static_cast<float*>(out), st);
+}
+
+}  // extern "C"
+
 // ------------------------------------------------------------------ no-alloc
 // Workspace of kvq3_decode_attn_noalloc: a fixed array in the library's
 // device image, so the call itself never allocates.  Every GPU that loads the

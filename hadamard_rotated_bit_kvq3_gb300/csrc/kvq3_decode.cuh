@@ -91,6 +91,7 @@ struct DecodeParams {
   int32_t pf_gkv;         // query heads per kv head
   int32_t pf_seq;         // the sequence
   int64_t pf_pos0;        // position of query token 0
+  int32_t out_half;       // the combine kernel writes fp16 (attention over selected pages)
 };
 
 // ------------------------------------------------------------------ helpers
@@ -1457,7 +1458,11 @@ __global__ void __launch_bounds__(256) decode_combine_kernel(const __grid_consta
     rotate_inverse<E, L>(o, rr, sgn, qt, qtr, p.inv_sqrt_d, so4, pair);
     if (grp == 0) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) out[(int64_t)it * D + rr * E + e] = o[e];
+      for (int e = 0; e < E; ++e) {
+        const int64_t at = (int64_t)it * D + rr * E + e;
+        if (p.out_half) reinterpret_cast<__half*>(out)[at] = __float2half_rn(o[e]);
+        else out[at] = o[e];
+      }
     }
   }
 }

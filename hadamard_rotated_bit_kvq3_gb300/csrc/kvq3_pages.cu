@@ -1,0 +1,463 @@
+// Page management of a paged cache: remapping sequences onto pages (fork,
+// reorder, grow, truncate, free) and compacting kept tokens into fresh pages.
+//
+// Remap.  The new table is a function of the old one: whole pages of a row's
+// source are shared, a part-filled page has one owner (the lowest row, unless
+// some row shares it whole) and is copied for the others, and the rest of the
+// entries take the lowest pages that no row of the new table holds.  Nothing
+// is kept between calls: which pages are free follows from the table itself,
+// so there are no reference counts to drift and the outcome does not depend
+// on the order of any atomic (the marks are bit-ors, the owner a minimum, the
+// free pages a rank over a bitmap).
+//
+// The bookkeeping is a chain of dependent passes over the table and the page
+// bitmap (a few hundred KB at most), bound by the latency of its barriers: one
+// thread-block cluster runs all of them with the hardware cluster barrier
+// between, in one launch.  The copies of part-filled pages are the only bulk
+// traffic; a second kernel, launched as its programmatic dependent, spreads
+// them over the GPU and moves only the slots in use.
+//
+// Compaction is a gather of packed vectors (codes and scales as stored); one
+// CTA takes a run of kept tokens of a (sequence, kv head), resolves each
+// token's record addresses once into shared memory, and moves the code strings
+// and scale headers with the widest accesses their sizes allow.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "kvq3_internal.h"
+
+namespace cg = cooperative_groups;
+using namespace kvq3;
+
+namespace {
+
+constexpr int kMapThreads = 1024;
+constexpr int kMapCluster = 8;      // CTAs of the remap cluster (the portable maximum)
+
+// What the remap keeps in its workspace.
+struct RemapWs {
+  uint32_t* bits;       // [ceil(num_pages / 32)] pages held by the new table
+  int32_t* owner;       // [num_pages] lowest row whose part-filled page it is (only such pages are written)
+  int32_t* freed;       // [num_pages] the lowest free pages in order
+  int32_t* need;        // [batch] entries a row takes from the free pages
+  int64_t* first;       // [batch] rank of the first of them
+  int4* rows;           // [batch] source row (-1: none), whole pages, tokens of the part-filled page, entries
+  int32_t* tail;        // [batch] the part-filled page's id, -1 where there is none
+  int4* copies;         // [batch] copy of a part-filled page: from, to, tokens (0: no copy)
+  size_t bytes;
+};
+
+RemapWs remap_layout(const CacheGeom& g, void* base) {
+  RemapWs w;
+  size_t at = 0;
+  auto take = [&](size_t n) {
+    const size_t o = at;
+    at += (n + 255) / 256 * 256;
+    return static_cast<char*>(base) + o;
+  };
+  const size_t n = (size_t)g.num_pages, b = (size_t)g.batch;
+  w.bits = reinterpret_cast<uint32_t*>(take((n + 31) / 32 * 4));
+  w.owner = reinterpret_cast<int32_t*>(take(n * 4));
+  w.freed = reinterpret_cast<int32_t*>(take(n * 4));
+  w.need = reinterpret_cast<int32_t*>(take(b * 4));
+  w.first = reinterpret_cast<int64_t*>(take(b * 8));
+  w.rows = reinterpret_cast<int4*>(take(b * 16));
+  w.tail = reinterpret_cast<int32_t*>(take(b * 4));
+  w.copies = reinterpret_cast<int4*>(take(b * 16));
+  w.bytes = at;
+  return w;
+}
+
+// Exclusive sum of v over the CTA's threads; *total receives the sum.
+__device__ __forceinline__ int64_t cta_excl(int64_t v, int64_t* wsum, int64_t* total) {
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  int64_t incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t t = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += t;
+  }
+  __syncthreads();
+  if (lane == 31) wsum[wid] = incl;
+  __syncthreads();
+  int64_t base = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kMapThreads / 32; ++w) {
+    const int64_t t = wsum[w];
+    base += w < wid ? t : 0;
+    all += t;
+  }
+  *total = all;
+  return base + incl - v;
+}
+
+__global__ void __launch_bounds__(kMapThreads)
+    remap_kernel(const __grid_constant__ CacheGeom g, const int32_t* table, const int32_t* seq_lens, const int32_t* src,
+                 const int32_t* new_lens, int32_t* table_out, int32_t* lens_out, const __grid_constant__ RemapWs ws,
+                 int32_t* status) {
+  __shared__ int64_t wsum[kMapThreads / 32];
+  __shared__ int64_t part[2];   // this CTA's free pages and wanted entries
+  griddep_wait();
+  griddep_launch_dependents();
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ncta = (int)cluster.num_blocks();
+  const int t = threadIdx.x, lane = t & 31;
+  const int64_t th = (int64_t)rank * kMapThreads + t, nth = (int64_t)ncta * kMapThreads;
+  const int64_t wp = th >> 5, nwp = nth >> 5;
+  const int64_t words = (g.num_pages + 31) / 32;
+  const int P = g.page_size;
+  const int64_t cap = (int64_t)g.max_pages * P;
+
+  // the rows, and an empty bitmap
+  for (int64_t i = th; i < words; i += nth) ws.bits[i] = 0;
+  for (int64_t b = th; b < g.batch; b += nth) {
+    const int s = src[b];
+    const int64_t want = new_lens[b];
+    int64_t held = 0, entries = 0;
+    int from = -1;
+    if (s < -1 || s >= g.batch) {
+      set_status(status, KVQ3_DEV_BAD_SEQ);
+    } else if (want < 0 || want > cap || (s >= 0 && (seq_lens[s] < 0 || seq_lens[s] > cap))) {
+      set_status(status, KVQ3_DEV_BAD_LEN);
+    } else {
+      from = s;
+      held = s >= 0 ? min((int64_t)seq_lens[s], want) : 0;
+      entries = (want + P - 1) / P;
+    }
+    const int full = (int)(held / P), rest = (int)(held % P);
+    int tail = -1;
+    if (rest) {
+      tail = table[(int64_t)from * g.max_pages + full];
+      if (tail < 0 || tail >= g.num_pages) {
+        set_status(status, KVQ3_DEV_BAD_PAGE);
+        tail = -1;
+      } else {
+        ws.owner[tail] = 0x7fffffff;
+      }
+    }
+    ws.rows[b] = make_int4(from, full, rest, (int)entries);
+    ws.tail[b] = tail;
+    ws.copies[b] = make_int4(0, 0, 0, 0);
+    lens_out[b] = (int32_t)held;
+  }
+  cluster.sync();
+  // whole pages are shared as they are
+  for (int64_t b = wp; b < g.batch; b += nwp) {
+    const int4 r = ws.rows[b];
+    for (int i = lane; i < g.max_pages; i += 32) {
+      int32_t page = -1;
+      if (i < r.y) {
+        page = table[(int64_t)r.x * g.max_pages + i];
+        if (page < 0 || page >= g.num_pages) {
+          set_status(status, KVQ3_DEV_BAD_PAGE);
+          page = -1;
+        } else {
+          atomicOr(&ws.bits[page >> 5], 1u << (page & 31));
+        }
+      }
+      table_out[b * g.max_pages + i] = page;
+    }
+  }
+  cluster.sync();
+  // owners of part-filled pages
+  for (int64_t b = th; b < g.batch; b += nth) {
+    const int tail = ws.tail[b];
+    if (tail >= 0) atomicMin(&ws.owner[tail], (int32_t)b);
+  }
+  cluster.sync();
+  for (int64_t b = th; b < g.batch; b += nth) {
+    const int4 r = ws.rows[b];
+    const int tail = ws.tail[b];
+    int keeps = 0;
+    if (tail >= 0 && ws.owner[tail] == b) {
+      // only the owner may set this bit here, so it is clear unless some row shares the page whole
+      const uint32_t bit = 1u << (tail & 31);
+      if ((atomicOr(&ws.bits[tail >> 5], bit) & bit) == 0) {
+        keeps = 1;
+        table_out[b * g.max_pages + r.y] = tail;
+        ws.tail[b] = -1;   // nothing to copy
+      }
+    }
+    // an unreadable part-filled page keeps its entry at -1
+    const int lost = r.z && tail < 0;
+    ws.need[b] = r.w - r.y - (keeps | lost);
+  }
+  cluster.sync();
+  // ranks: every CTA counts the free pages and the wanted entries of its slice
+  const int64_t w0 = words * rank / ncta, w1 = words * (rank + 1) / ncta;
+  const int64_t b0 = (int64_t)g.batch * rank / ncta, b1 = (int64_t)g.batch * (rank + 1) / ncta;
+  auto free_of = [&](int64_t w) {
+    uint32_t f = ~__ldcg(&ws.bits[w]);
+    if (w == words - 1 && (g.num_pages & 31)) f &= (1u << (g.num_pages & 31)) - 1u;
+    return f;
+  };
+  {
+    int64_t f = 0, n = 0, total;
+    for (int64_t w = w0 + t; w < w1; w += kMapThreads) f += __popc(free_of(w));
+    for (int64_t b = b0 + t; b < b1; b += kMapThreads) n += ws.need[b];
+    cta_excl(f, wsum, &total);
+    if (t == 0) part[0] = total;
+    cta_excl(n, wsum, &total);
+    if (t == 0) part[1] = total;
+  }
+  cluster.sync();
+  int64_t free_before = 0, want_before = 0, free_all = 0, want_all = 0;
+  for (int c = 0; c < ncta; ++c) {
+    const int64_t* other = cluster.map_shared_rank(part, c);
+    const int64_t f = other[0], n = other[1];
+    if (c < rank) {
+      free_before += f;
+      want_before += n;
+    }
+    free_all += f;
+    want_all += n;
+  }
+  const bool enough = want_all <= free_all;
+  if (!enough && th == 0) set_status(status, KVQ3_DEV_NO_PAGE);
+  // the slice's free pages below the number wanted, in order
+  for (int64_t base = w0; base < w1 && free_before < want_all; base += kMapThreads) {
+    const int64_t w = base + t;
+    uint32_t f = w < w1 ? free_of(w) : 0u;
+    int64_t total;
+    int64_t at = free_before + cta_excl(__popc(f), wsum, &total);
+    while (f && at < want_all) {
+      ws.freed[at++] = (int32_t)(w * 32 + __ffs(f) - 1);
+      f &= f - 1;
+    }
+    free_before += total;
+  }
+  for (int64_t base = b0; base < b1; base += kMapThreads) {
+    const int64_t b = base + t;
+    int64_t total;
+    const int64_t at = want_before + cta_excl(b < b1 ? ws.need[b] : 0, wsum, &total);
+    if (b < b1) ws.first[b] = at;
+    want_before += total;
+  }
+  cluster.sync();   // also: no CTA leaves while another reads its shared memory
+  if (!enough) return;
+  for (int64_t b = wp; b < g.batch; b += nwp) {
+    const int4 r = ws.rows[b];
+    const int n = ws.need[b];
+    const int64_t at = ws.first[b];
+    const int tail = ws.tail[b];
+    for (int i = lane; i < n; i += 32) {
+      const int32_t page = ws.freed[at + i];
+      table_out[b * g.max_pages + r.w - n + i] = page;
+      if (i == 0 && tail >= 0) ws.copies[b] = make_int4(tail, page, r.z, 0);
+    }
+  }
+}
+
+// Copies `bytes` bytes (a multiple of any size) from src to dst, both 16-byte
+// aligned, over the CTA's threads.
+__device__ __forceinline__ void cta_copy(uint8_t* dst, const uint8_t* src, int64_t bytes) {
+  const int64_t n = bytes / 16;
+  for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
+    reinterpret_cast<uint4*>(dst)[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i);
+  for (int64_t i = n * 16 + threadIdx.x; i < bytes; i += blockDim.x) dst[i] = src[i];
+}
+
+__global__ void __launch_bounds__(256)
+    remap_copy_kernel(const __grid_constant__ CacheGeom g, uint8_t* pool, const int4* copies, int32_t* status) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int recs = 2 * g.hkv;
+  const int64_t items = (int64_t)g.batch * recs;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t b = it / recs;
+    const int4 c = copies[b];
+    if (c.z == 0) continue;
+    const int64_t rec = (it - b * recs) * g.record_bytes;
+    const int64_t from = c.x * g.page_bytes + rec, to = c.y * g.page_bytes + rec;
+    if (!KVQ3_CHECK(status, in_range(from, g.record_bytes, g.num_pages * g.page_bytes) &&
+                                in_range(to, g.record_bytes, g.num_pages * g.page_bytes)))
+      continue;
+    cta_copy(pool + to, pool + from, (int64_t)c.z * g.nb * g.sb);
+    cta_copy(pool + to + g.scale_hdr_bytes, pool + from + g.scale_hdr_bytes, (int64_t)c.z * g.cb);
+  }
+}
+
+// ------------------------------------------------------------ compaction
+constexpr int kKeepTile = 256;   // kept tokens per CTA
+
+// CV: bytes of a code access (16 or 8, dividing a code string); HV: bytes of a
+// header access (dividing a token's scales).
+template <typename CV, typename HV>
+__global__ void __launch_bounds__(kKeepTile)
+    compact_kernel(const __grid_constant__ CacheGeom g, uint8_t* pool, const int32_t* __restrict__ page_table,
+                   const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ src_seq,
+                   const int32_t* __restrict__ dst_seq, const int32_t* __restrict__ keep,
+                   const int32_t* __restrict__ n_keep, int keep_stride, int tiles, int32_t* status) {
+  __shared__ int64_t from_s[kKeepTile], to_s[kKeepTile];   // K records, -1: skip
+  __shared__ int32_t slots_s[kKeepTile];                   // source slot, destination slot << 16
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = threadIdx.x;
+  const int64_t unit = blockIdx.x / tiles;
+  const int tile = (int)(blockIdx.x - unit * tiles);
+  const int i = (int)(unit / g.hkv), kvh = (int)(unit - (int64_t)i * g.hkv);
+  const int64_t cap = (int64_t)g.max_pages * g.page_size;
+  const int s = src_seq[i], d = dst_seq[i], n = n_keep[i];
+  int bad = 0;
+  int64_t len = 0;
+  if (s < 0 || s >= g.batch || d < 0 || d >= g.batch || s == d) bad = KVQ3_DEV_BAD_SEQ;
+  else {
+    len = seq_lens[s];
+    if (len < 0 || len > cap || n < 0 || n > keep_stride || n > cap) bad = KVQ3_DEV_BAD_LEN;
+  }
+  if (bad) {
+    if (t == 0) set_status(status, bad);
+    return;
+  }
+  const int64_t t0 = (int64_t)tile * kKeepTile;
+  const int m = (int)min((int64_t)kKeepTile, n - t0);
+  if (m <= 0) return;
+  if (t < m) {
+    const int64_t at = t0 + t;
+    const int64_t pos = keep[unit * keep_stride + at];
+    int64_t a = -1, z = -1;
+    if (pos < 0 || pos >= len) {
+      set_status(status, KVQ3_DEV_BAD_POS);
+    } else {
+      const int64_t ps = page_of(g, page_table, s, pos / g.page_size), pd = page_of(g, page_table, d, at / g.page_size);
+      if (ps < 0 || pd < 0) set_status(status, KVQ3_DEV_BAD_PAGE);
+      else {
+        a = record_offset(g, ps, kvh, 0);
+        z = record_offset(g, pd, kvh, 0);
+        slots_s[t] = (int32_t)(pos % g.page_size) | ((int32_t)(at % g.page_size) << 16);
+        if (!KVQ3_CHECK(status, in_range(a, 2 * g.record_bytes, g.num_pages * g.page_bytes) &&
+                                    in_range(z, 2 * g.record_bytes, g.num_pages * g.page_bytes)))
+          a = -1;
+      }
+    }
+    from_s[t] = a;
+    to_s[t] = z;
+  }
+  __syncthreads();
+  const int hb = g.nb * g.sb;
+  const int cn = g.cb / (int)sizeof(CV), hn = hb / (int)sizeof(HV);
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    const int64_t rec = which * g.record_bytes;
+    for (int k = t; k < m * cn; k += kKeepTile) {
+      const int tok = k / cn, e = k - tok * cn;
+      const int64_t a = from_s[tok];
+      if (a < 0) continue;
+      const int sl = slots_s[tok];
+      reinterpret_cast<CV*>(pool + to_s[tok] + rec + g.scale_hdr_bytes + (int64_t)(sl >> 16) * g.cb)[e] =
+          reinterpret_cast<const CV*>(pool + a + rec + g.scale_hdr_bytes + (int64_t)(sl & 0xffff) * g.cb)[e];
+    }
+    for (int k = t; k < m * hn; k += kKeepTile) {
+      const int tok = k / hn, e = k - tok * hn;
+      const int64_t a = from_s[tok];
+      if (a < 0) continue;
+      const int sl = slots_s[tok];
+      reinterpret_cast<HV*>(pool + to_s[tok] + rec + (int64_t)(sl >> 16) * hb)[e] =
+          reinterpret_cast<const HV*>(pool + a + rec + (int64_t)(sl & 0xffff) * hb)[e];
+    }
+  }
+}
+
+template <typename CV, typename HV>
+cudaError_t launch_compact(const CacheGeom& g, const kvq3_cache* c, const int32_t* src_seq, const int32_t* dst_seq,
+                           int64_t units, const int32_t* keep, const int32_t* n_keep, int keep_stride, int32_t* st,
+                           cudaStream_t stream) {
+  const int tiles = (int)(((int64_t)keep_stride + kKeepTile - 1) / kKeepTile);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * tiles));
+  cfg.blockDim = dim3(kKeepTile);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, compact_kernel<CV, HV>, g, static_cast<uint8_t*>(c->pool), c->page_table, c->seq_lens,
+                            src_seq, dst_seq, keep, n_keep, keep_stride, tiles, st);
+}
+
+template <typename CV>
+cudaError_t compact_by_header(const CacheGeom& g, const kvq3_cache* c, const int32_t* src_seq, const int32_t* dst_seq,
+                              int64_t units, const int32_t* keep, const int32_t* n_keep, int keep_stride, int32_t* st,
+                              cudaStream_t stream) {
+  switch (g.nb * g.sb) {   // a power of two: 1 to 32 bytes
+    case 1: return launch_compact<CV, uint8_t>(g, c, src_seq, dst_seq, units, keep, n_keep, keep_stride, st, stream);
+    case 2: return launch_compact<CV, uint16_t>(g, c, src_seq, dst_seq, units, keep, n_keep, keep_stride, st, stream);
+    case 4: return launch_compact<CV, uint32_t>(g, c, src_seq, dst_seq, units, keep, n_keep, keep_stride, st, stream);
+    case 8: return launch_compact<CV, uint2>(g, c, src_seq, dst_seq, units, keep, n_keep, keep_stride, st, stream);
+    default: return launch_compact<CV, uint4>(g, c, src_seq, dst_seq, units, keep, n_keep, keep_stride, st, stream);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+kvq3_status kvq3_remap_workspace_size(const kvq3_cache_desc* desc, size_t* bytes) {
+  CacheGeom g;
+  const kvq3_status s = make_geom(desc, &g);
+  if (s != KVQ3_OK) return s;
+  if (!bytes) return KVQ3_ERR_INVALID_ARG;
+  if (g.num_pages >= ((int64_t)1 << 31)) return KVQ3_ERR_UNSUPPORTED;   // int32 page ids
+  *bytes = remap_layout(g, nullptr).bytes;
+  return KVQ3_OK;
+}
+
+kvq3_status kvq3_remap(const kvq3_cache_desc* desc, const kvq3_cache* cache, const int32_t* src, const int32_t* new_lens,
+                       int32_t* table_out, int32_t* lens_out, void* workspace, size_t ws_bytes, int32_t* dev_status,
+                       void* stream) {
+  CacheGeom g;
+  kvq3_status s = make_geom(desc, &g);
+  if (s != KVQ3_OK) return s;
+  if ((s = check_cache(g, cache, true)) != KVQ3_OK) return s;
+  if (!cache->page_table || !src || !new_lens || !table_out || !lens_out || table_out == cache->page_table ||
+      lens_out == cache->seq_lens)
+    return KVQ3_ERR_INVALID_ARG;
+  if (g.num_pages >= ((int64_t)1 << 31)) return KVQ3_ERR_UNSUPPORTED;
+  const RemapWs ws = remap_layout(g, workspace);
+  if (!workspace || ws_bytes < ws.bytes || reinterpret_cast<uintptr_t>(workspace) % 256) return KVQ3_ERR_WORKSPACE;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kMapCluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kMapCluster);
+  cfg.blockDim = dim3(kMapThreads);
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, remap_kernel, g, cache->page_table, cache->seq_lens, src, new_lens, table_out, lens_out,
+                         ws, dev_status) != cudaSuccess)
+    return KVQ3_ERR_CUDA;
+  const int64_t items = (int64_t)g.batch * 2 * g.hkv, cap = (int64_t)sm_count() * 8;
+  cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min(items, cap)));
+  cfg.blockDim = dim3(256);
+  cfg.numAttrs = 1;
+  return cuda_status(cudaLaunchKernelEx(&cfg, remap_copy_kernel, g, static_cast<uint8_t*>(cache->pool),
+                                        static_cast<const int4*>(ws.copies), dev_status));
+}
+
+kvq3_status kvq3_compact(const kvq3_cache_desc* desc, const kvq3_cache* cache, const int32_t* src_seq,
+                         const int32_t* dst_seq, int32_t n_seq, const int32_t* keep, const int32_t* n_keep,
+                         int32_t keep_stride, int32_t* dev_status, void* stream) {
+  CacheGeom g;
+  kvq3_status s = make_geom(desc, &g);
+  if (s != KVQ3_OK) return s;
+  if ((s = check_cache(g, cache, true)) != KVQ3_OK) return s;
+  if (n_seq < 0 || keep_stride < 0) return KVQ3_ERR_INVALID_ARG;
+  if (n_seq == 0 || keep_stride == 0) return KVQ3_OK;
+  if (!src_seq || !dst_seq || !keep || !n_keep) return KVQ3_ERR_INVALID_ARG;
+  const int64_t units = (int64_t)n_seq * g.hkv, tiles = ((int64_t)keep_stride + kKeepTile - 1) / kKeepTile;
+  if (units >= ((int64_t)1 << 31) / tiles) return KVQ3_ERR_UNSUPPORTED;   // one CTA per tile
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // a code string is a multiple of 16 bytes except at d = 64 with 3-bit codes (24)
+  const cudaError_t e = g.cb % 16 == 0
+      ? compact_by_header<uint4>(g, cache, src_seq, dst_seq, units, keep, n_keep, keep_stride, dev_status, st)
+      : compact_by_header<uint2>(g, cache, src_seq, dst_seq, units, keep, n_keep, keep_stride, dev_status, st);
+  return cuda_status(e);
+}
+
+}  // extern "C"

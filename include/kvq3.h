@@ -171,6 +171,7 @@ enum {
   KVQ3_DEV_BAD_LEN = 8,      /* seq_lens[b] outside [0, capacity] */
   KVQ3_DEV_BAD_CODE = 16,    /* a stored code of -2^(b-1), e.g. -4 at b = 3 (never written) */
   KVQ3_DEV_TIMEOUT = 32,     /* an asynchronous copy did not arrive in time */
+  KVQ3_DEV_NO_PAGE = 128,    /* fewer free pages than a remap needs */
   KVQ3_DEV_CHECK = 64        /* a bounds check of a checked build failed (the
                                 library compiled with KVQ3_CHECKED); the
                                 access was skipped */
@@ -445,6 +446,136 @@ kvq3_status kvq3_calibrate_so4_pair(kvq3_rotation rot, const kvq3_cache_desc *de
                                     int64_t n, int32_t rounds, int32_t num_candidates, float step,
                                     uint64_t seed, void *workspace, size_t ws_bytes, float *quats_out,
                                     float *quats_r_out, double *sse_out, void *stream);
+
+/* ---- Sparse decode: attention over the pages that a cheap score selects (none
+ * of the pages has a counterpart; the method's cache, read path and rotation
+ * are kept).  A serving loop calls, per step: kvq3_write, kvq3_key_bounds for
+ * the newest position, kvq3_page_scores, kvq3_page_select and
+ * kvq3_decode_attn_pages.  "Page i" of a sequence is its logical page i, the
+ * positions [i*P, (i+1)*P).
+ *
+ * kvq3_key_bounds: elementwise minimum and maximum of the dequantised rotated
+ * keys of each page, over the page's positions below seq_lens[b], for every
+ * page of every sequence b that holds a position in [first_pos[b],
+ * seq_lens[b]) (first_pos NULL: every page; a page is always summarised whole,
+ * from its first position).  bounds: device fp16 [num_pages][Hkv][2][d]
+ * (minimum, then maximum; indexed by physical page), 16-byte aligned; entries
+ * of other pages are left as they were.  Each bound is the exact value rounded
+ * to fp16 (fp32 scales: the fp32 product rounded to fp16), so dequantised keys
+ * must lie in the fp16 range, as for the attention.  A page that two
+ * sequences share must be whole in both, as kvq3_remap leaves it.
+ * first_pos: device int32 [batch].  A length outside [0, capacity] or a
+ * negative first_pos skips the sequence (KVQ3_DEV_BAD_LEN), a bad page id the
+ * page (KVQ3_DEV_BAD_PAGE). */
+kvq3_status kvq3_key_bounds(const kvq3_cache_desc *desc, const kvq3_cache *cache,
+                            const int32_t *first_pos, void *bounds, int32_t *dev_status,
+                            void *stream);
+
+/* Scores of a decode step's queries against each page's key bounds: with
+ * q1 = U q, scores[b][h][i] = max over the Hq/Hkv query heads of kv head h of
+ * sum_j max(q1_j lo_j, q1_j hi_j), page i of sequence b.  Up to the fp16
+ * rounding of the bounds that is at least every q1 . k_hat of the page (the
+ * logits before sm_scale).  Entries of pages at or past seq_lens[b], of a
+ * sequence with a bad length (KVQ3_DEV_BAD_LEN) and of bad page ids
+ * (KVQ3_DEV_BAD_PAGE) are -infinity.
+ * q: device fp16 [batch][Hq][d], 16-byte aligned; bounds: device fp16
+ * [num_pages][Hkv][2][d], 16-byte aligned; scores: device fp32
+ * [batch][Hkv][max_pages_per_seq], every entry written. */
+kvq3_status kvq3_page_scores(kvq3_rotation rot, const kvq3_cache_desc *desc,
+                             const kvq3_cache *cache, const void *bounds, const void *q,
+                             int32_t num_q_heads, float *scores, int32_t *dev_status,
+                             void *stream);
+
+/* The pages each (sequence, kv head) attends to: all of them when the
+ * sequence has at most `budget`, else its first `sinks` pages, its last
+ * `recent` pages and, of those between, the budget - sinks - recent with the
+ * highest scores (equal scores: the lower page; NaN counts as the lowest).
+ * pages: device int32 [batch][Hkv][budget], ascending, then -1; counts:
+ * device int32 [batch][Hkv].  Only seq_lens of the cache is read.  budget >=
+ * 1, sinks >= 0, recent >= 1 (the page being written is always attended) and
+ * sinks + recent <= budget, else KVQ3_ERR_INVALID_ARG.  A sequence with a bad
+ * length gets no pages (KVQ3_DEV_BAD_LEN). */
+kvq3_status kvq3_page_select(const kvq3_cache_desc *desc, const kvq3_cache *cache,
+                             const float *scores, int32_t budget, int32_t sinks, int32_t recent,
+                             int32_t *pages, int32_t *counts, int32_t *dev_status, void *stream);
+
+/* Device workspace bytes of kvq3_decode_attn_pages with lists of up to
+ * max_selected pages. */
+kvq3_status kvq3_decode_pages_workspace_size(const kvq3_cache_desc *desc, int32_t num_q_heads,
+                                             int32_t max_selected, size_t *bytes);
+
+/* kvq3_decode_attn over selected pages: each query head of kv head h of
+ * sequence b attends to the positions below seq_lens[b] of the pages
+ * pages[b][h][0 .. counts[b][h]).  pages: device int32
+ * [batch][Hkv][max_selected], strictly ascending (as kvq3_page_select writes
+ * them); counts: device int32 [batch][Hkv], 0 <= counts <= max_selected.
+ * A list entry that is not a page of the sequence or not above the entry
+ * before it is left out (KVQ3_DEV_BAD_PAGE); a bad count or length gives zeros
+ * (KVQ3_DEV_BAD_LEN), and so does an empty list.
+ * q: device fp16 [batch][Hq][d]; out: device fp16 [batch][Hq][d], what the
+ * projection after it reads (one rounding of the fp32 result, 2^-11 relative,
+ * below the error bar of the attention).  workspace: device, 256-byte
+ * aligned, ws_bytes >= kvq3_decode_pages_workspace_size; calls sharing it must
+ * not overlap.  The rest as for kvq3_decode_attn; KVQ3_ERR_UNSUPPORTED when
+ * num_pages * Hkv, batch * Hq or max_selected * P reaches 2^31. */
+kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc *desc,
+                                   const kvq3_cache *cache, const void *q, int32_t num_q_heads,
+                                   float sm_scale, const int32_t *pages, const int32_t *counts,
+                                   int32_t max_selected, void *out, void *workspace,
+                                   size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/* ---- Pages of a paged cache: forking, growing, truncating, freeing and
+ * compacting sequences (a page table is required).
+ *
+ * kvq3_remap: the page table after a step, as a function of the one before.
+ * Sequence b continues the first held[b] = min(seq_lens[src[b]], new_lens[b])
+ * tokens of sequence src[b] (src[b] = -1: none) and gets pages for new_lens[b]
+ * tokens: src[b] = b grows or truncates a sequence, another source forks or
+ * reorders (beam search, a shared prefix), new_lens[b] = 0 frees.
+ *   - Pages that a sequence holds whole are shared, never copied.
+ *   - A page it holds in part (the last one, when held[b] is not a multiple
+ *     of P) is kept by the lowest such row b, unless another row shares it
+ *     whole; every other row gets a copy of the tokens it holds, in a page of
+ *     its own.  So the page a sequence appends to is never shared.
+ *   - The remaining entries, row by row, take the lowest-numbered free pages.
+ *     A page is free when no row of the new table holds it: there is no other
+ *     allocation state, and a page held outside the table (a kept prefix)
+ *     is one that some row of the batch holds.
+ * table_out: device int32 [batch][max_pages_per_seq], not the cache's table
+ * (KVQ3_ERR_INVALID_ARG), -1 past new_lens[b]; lens_out: device int32
+ * [batch] = held, not the cache's lengths.  The caller then uses the two in
+ * place of the cache's page_table and seq_lens.  Contents of a page beyond
+ * the tokens it held are left as they were; key bounds of a copied page are
+ * not copied (kvq3_key_bounds makes them).
+ * With too few free pages nothing is copied, the entries without a page are
+ * -1 and KVQ3_DEV_NO_PAGE is set: the old table and lengths are still valid.
+ * src[b] outside [-1, batch) (KVQ3_DEV_BAD_SEQ), a source length or
+ * new_lens[b] outside [0, capacity] (KVQ3_DEV_BAD_LEN) frees row b; a bad
+ * page id of the old table gives -1 (KVQ3_DEV_BAD_PAGE).
+ * workspace: device, 256-byte aligned, ws_bytes >=
+ * kvq3_remap_workspace_size; calls sharing it must not overlap. */
+kvq3_status kvq3_remap_workspace_size(const kvq3_cache_desc *desc, size_t *bytes);
+kvq3_status kvq3_remap(const kvq3_cache_desc *desc, const kvq3_cache *cache, const int32_t *src,
+                       const int32_t *new_lens, int32_t *table_out, int32_t *lens_out,
+                       void *workspace, size_t ws_bytes, int32_t *dev_status, void *stream);
+
+/* Gathers kept tokens of sequences into other sequences of the cache, as
+ * stored (codes and scales, no requantisation): for i < n_seq, kv head h and
+ * t < n_keep[i], position t of sequence dst_seq[i] becomes position
+ * keep[i][h][t] of sequence src_seq[i], keys and values.  Heads may keep
+ * different positions, in any order and more than once.  The destination's
+ * pages must be there (kvq3_remap with src = -1) and be nobody's source; its
+ * length is the caller's to set.  keep: device int32 [n_seq][Hkv][keep_stride];
+ * src_seq, dst_seq, n_keep: device int32 [n_seq].  A destination named twice
+ * gets a mixture of the two.  An entry outside the source's length leaves its
+ * slot as it was (KVQ3_DEV_BAD_POS); sequence ids out of range or equal skip
+ * the pair (KVQ3_DEV_BAD_SEQ), n_keep outside [0, min(keep_stride, capacity)]
+ * or a bad source length too (KVQ3_DEV_BAD_LEN); bad page ids skip their
+ * tokens (KVQ3_DEV_BAD_PAGE). */
+kvq3_status kvq3_compact(const kvq3_cache_desc *desc, const kvq3_cache *cache,
+                         const int32_t *src_seq, const int32_t *dst_seq, int32_t n_seq,
+                         const int32_t *keep, const int32_t *n_keep, int32_t keep_stride,
+                         int32_t *dev_status, void *stream);
 
 #ifdef __cplusplus
 }
