@@ -64,6 +64,25 @@ kvq3_status prefill_run_for(const CacheGeom& g, const DecodePlan& plan, const De
   return KVQ3_ERR_UNSUPPORTED;
 }
 
+kvq3_status pages_plan_for(const CacheGeom& g, int G, DecodePlan* plan) {
+  switch (g.d) {
+    case 64: KVQ3_BY_SCALE(64, pages_plan, g, G, plan)
+    case 128: KVQ3_BY_SCALE(128, pages_plan, g, G, plan)
+    case 256: KVQ3_BY_SCALE(256, pages_plan, g, G, plan)
+  }
+  return KVQ3_ERR_UNSUPPORTED;
+}
+
+kvq3_status pages_run_for(const CacheGeom& g, const DecodePlan& plan, const DecodeParams& prm,
+                          const RotParams& rp, cudaStream_t st) {
+  switch (g.d) {
+    case 64: KVQ3_BY_SCALE(64, pages_run, plan, prm, rp, st)
+    case 128: KVQ3_BY_SCALE(128, pages_run, plan, prm, rp, st)
+    case 256: KVQ3_BY_SCALE(256, pages_run, plan, prm, rp, st)
+  }
+  return KVQ3_ERR_UNSUPPORTED;
+}
+
 kvq3_status check_heads(const CacheGeom& g, int32_t hq) {
   if (hq < 1 || hq % g.hkv != 0) return KVQ3_ERR_INVALID_ARG;
   if (hq / g.hkv > 16) return KVQ3_ERR_UNSUPPORTED;
@@ -283,8 +302,11 @@ kvq3_status kvq3_test_prefill_attn_polls(kvq3_rotation rot, const kvq3_cache_des
 }  // extern "C"
 
 // ------------------------------------------------------------------ selected pages
-// Attention over selected pages runs the decode kernel on another view of the
-// same pool: a record pair (K and V of one page and kv head) is a page of its
+// Attention over selected pages has two forms.  The cluster form (SEL of the
+// decode kernel) is one launch: 1 to 8 CTAs per (sequence, kv head), merged
+// through the cluster's shared memory.  Where there are so few units, with
+// lists so long, that 8 CTAs a unit leave most of the GPU idle, the flattened
+// form runs the dense decode kernel on another view of the same pool: a record pair (K and V of one page and kv head) is a page of its
 // own, number page * Hkv + kv head, and every (sequence, kv head) a sequence
 // of one kv head whose page table is its list.  The list is ascending, so only
 // its last page can be part filled, and the view's length says how far.
@@ -347,6 +369,35 @@ kvq3_status pages_view(const CacheGeom& g, int32_t hq, int32_t row, CacheGeom* v
   return KVQ3_OK;
 }
 
+// CTAs per unit of the cluster form, 0 for the flattened one.  The costs are in
+// units of one chunk's time on a busy SM (1.1 to 1.3 us): a wave of CTAs pays
+// about 6.5 to start and to merge, an SM needs about 2.4 chunks in flight to
+// be busy, and the flattened form pays about 26 for its list, partials and
+// second kernel but divides the chunks evenly over all CTAs.  Measured (us),
+// 128 units of 16 chunks at 4 CTAs an SM: 1, 2, 3, 4, 8 CTAs a unit 43.4,
+// 27.5, 32.9, 25.6, 30.2, flattened 39.6; 64 units of 64 chunks at 3 an SM: 4,
+// 5, 6, 8 CTAs 67.8, 58.9, 51.0, 69.0, flattened 65.3.
+int pages_parts(const DecodePlan& plan, int64_t units, int32_t row) {
+  const int sms = std::max(1, sm_count());
+  const int per_sm = std::max(1, plan.ctas / sms);
+  const int64_t nc = ((int64_t)row + plan.pages_per_chunk - 1) / plan.pages_per_chunk;
+  double best = 26.0 + std::max(2.4, (double)per_sm) * (double)((units * nc + plan.ctas - 1) / plan.ctas);
+  int parts = 0;
+  for (int n = 1; n <= 8 && n <= nc; ++n) {
+    if (plan.clusters[n] < 1) continue;
+    const int64_t waves = (units + plan.clusters[n] - 1) / plan.clusters[n];
+    const int64_t last = units - (waves - 1) * plan.clusters[n];   // clusters of the last wave
+    const double k = (double)((nc + n - 1) / n);
+    const double cost = waves * 6.5 + (waves - 1) * k * std::max(2.4, (double)per_sm) +
+                        k * std::max(2.4, (double)((last * n + sms - 1) / sms));
+    if (cost < best) {
+      best = cost;
+      parts = n;
+    }
+  }
+  return parts;
+}
+
 // Bytes of the view's table and lengths ahead of the decode workspace.
 size_t view_bytes(const CacheGeom& v) { return ((size_t)v.batch * ((size_t)v.max_pages + 1) * 4 + 255) / 256 * 256; }
 
@@ -361,16 +412,20 @@ kvq3_status kvq3_decode_pages_workspace_size(const kvq3_cache_desc* desc, int32_
   if (s != KVQ3_OK) return s;
   if (!bytes) return KVQ3_ERR_INVALID_ARG;
   if ((s = pages_view(g, num_q_heads, max_selected, &v)) != KVQ3_OK) return s;
+  const int G = num_q_heads / g.hkv;
   DecodePlan plan;
-  if ((s = plan_for(v, num_q_heads / g.hkv, &plan)) != KVQ3_OK) return s;
+  if ((s = pages_plan_for(g, G, &plan)) != KVQ3_OK) return s;
+  *bytes = 256;   // the cluster form needs none
+  if (pages_parts(plan, v.batch, max_selected) > 0) return KVQ3_OK;
+  if ((s = plan_for(v, G, &plan)) != KVQ3_OK) return s;
   *bytes = view_bytes(v) + plan.ws_bytes;
   return KVQ3_OK;
 }
 
-kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc* desc, const kvq3_cache* cache,
-                                   const void* q, int32_t num_q_heads, float sm_scale, const int32_t* pages,
-                                   const int32_t* counts, int32_t max_selected, void* out, void* workspace,
-                                   size_t ws_bytes, int32_t* dev_status, void* stream) {
+static kvq3_status decode_pages_impl(kvq3_rotation rot, const kvq3_cache_desc* desc, const kvq3_cache* cache,
+                                     const void* q, int32_t num_q_heads, float sm_scale, const int32_t* pages,
+                                     const int32_t* counts, int32_t max_selected, void* out, void* workspace,
+                                     size_t ws_bytes, int32_t* dev_status, void* stream, uint32_t wait_limit) {
   CacheGeom g, v;
   kvq3_status s = make_geom(desc, &g);
   if (s != KVQ3_OK) return s;
@@ -378,17 +433,42 @@ kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc* des
   if ((s = check_cache(g, cache, true)) != KVQ3_OK) return s;
   if ((s = pages_view(g, num_q_heads, max_selected, &v)) != KVQ3_OK) return s;
   if (!(sm_scale <= 0.0f || isfinite(sm_scale))) return KVQ3_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) % 16 != 0) return KVQ3_ERR_INVALID_ARG;
   const int G = num_q_heads / g.hkv;
   DecodePlan plan;
-  if ((s = plan_for(v, G, &plan)) != KVQ3_OK) return s;
+  if ((s = pages_plan_for(g, G, &plan)) != KVQ3_OK) return s;
+  const int parts = pages_parts(plan, v.batch, max_selected);
+  if (parts == 0 && (s = plan_for(v, G, &plan)) != KVQ3_OK) return s;
   const size_t head = view_bytes(v);
-  if (!workspace || ws_bytes < head + plan.ws_bytes || reinterpret_cast<uintptr_t>(workspace) % 256)
+  if (!workspace || ws_bytes < (parts ? 256 : head + plan.ws_bytes) || reinterpret_cast<uintptr_t>(workspace) % 256)
     return KVQ3_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  DecodeParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.pool = static_cast<const uint8_t*>(cache->pool);
+  prm.q = static_cast<const __half*>(q);
+  prm.status = dev_status;
+  prm.G = G;
+  const double sc = sm_scale > 0.0f ? (double)sm_scale : 1.0 / sqrt((double)g.d);
+  prm.qk_scale = (float)(sc * 1.4426950408889634);  // log2(e): softmax in base 2
+  prm.inv_sqrt_d = inv_sqrt(g.d);
+  prm.wait_limit = wait_limit;
+  if (parts > 0) {
+    prm.g = g;
+    prm.page_table = cache->page_table;
+    prm.seq_lens = cache->seq_lens;
+    prm.Hq = num_q_heads;
+    prm.sel_pages = pages;
+    prm.sel_counts = counts;
+    prm.sel_row = max_selected;
+    prm.sel_parts = parts;
+    prm.sel_out = static_cast<__half*>(out);
+    return pages_run_for(g, plan, prm, rot->params, st);
+  }
+
   int32_t* vtable = static_cast<int32_t*>(workspace);
   int32_t* vlens = vtable + (size_t)v.batch * v.max_pages;
   char* ws = static_cast<char*>(workspace) + head;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -402,26 +482,34 @@ kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc* des
   if (cudaLaunchKernelEx(&cfg, page_list_kernel, g, cache->page_table, cache->seq_lens, pages, counts, max_selected,
                          vtable, vlens, dev_status) != cudaSuccess)
     return KVQ3_ERR_CUDA;
-
-  DecodeParams prm;
-  memset(&prm, 0, sizeof(prm));
   prm.g = v;
-  prm.pool = static_cast<const uint8_t*>(cache->pool);
   prm.page_table = vtable;
   prm.seq_lens = vlens;
-  prm.q = static_cast<const __half*>(q);
   prm.ws = reinterpret_cast<float*>(ws);
   prm.unit_cta = reinterpret_cast<int32_t*>(ws + ((size_t)plan.ctas + (size_t)v.batch) * G * (g.d + 2) * sizeof(float));
-  prm.status = dev_status;
-  prm.G = G;
   prm.Hq = G;
-  const double sc = sm_scale > 0.0f ? (double)sm_scale : 1.0 / sqrt((double)g.d);
-  prm.qk_scale = (float)(sc * 1.4426950408889634);  // log2(e): softmax in base 2
-  prm.inv_sqrt_d = inv_sqrt(g.d);
   prm.slot_floats = (uint32_t)(G * (g.d + 2));
-  prm.wait_limit = kWaitPolls;
   prm.out_half = 1;
   return run_for(v, plan, prm, rot->params, static_cast<float*>(out), st);
+}
+
+kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc* desc, const kvq3_cache* cache,
+                                   const void* q, int32_t num_q_heads, float sm_scale, const int32_t* pages,
+                                   const int32_t* counts, int32_t max_selected, void* out, void* workspace,
+                                   size_t ws_bytes, int32_t* dev_status, void* stream) {
+  return decode_pages_impl(rot, desc, cache, q, num_q_heads, sm_scale, pages, counts, max_selected, out, workspace,
+                           ws_bytes, dev_status, stream, kWaitPolls);
+}
+
+// Test hook, not part of the public header: kvq3_decode_attn_pages with the
+// bound on each stage wait set to `polls` mbarrier polls, as
+// kvq3_test_decode_attn_polls.
+kvq3_status kvq3_test_decode_pages_polls(kvq3_rotation rot, const kvq3_cache_desc* desc, const kvq3_cache* cache,
+                                         const void* q, int32_t num_q_heads, float sm_scale, const int32_t* pages,
+                                         const int32_t* counts, int32_t max_selected, void* out, void* workspace,
+                                         size_t ws_bytes, int32_t* dev_status, void* stream, uint32_t polls) {
+  return decode_pages_impl(rot, desc, cache, q, num_q_heads, sm_scale, pages, counts, max_selected, out, workspace,
+                           ws_bytes, dev_status, stream, polls);
 }
 
 }  // extern "C"

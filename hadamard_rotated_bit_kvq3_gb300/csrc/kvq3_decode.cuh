@@ -91,7 +91,15 @@ struct DecodeParams {
   int32_t pf_gkv;         // query heads per kv head
   int32_t pf_seq;         // the sequence
   int64_t pf_pos0;        // position of query token 0
-  int32_t out_half;       // the combine kernel writes fp16 (attention over selected pages)
+  // Attention over selected pages: the (sequence, kv head) unit u attends to
+  // the pages sel_pages[u][0 .. sel_counts[u]) of its sequence, sel_parts CTAs
+  // (one cluster) sharing the list; the fp16 result goes to sel_out.
+  const int32_t* sel_pages;   // [units][sel_row]
+  const int32_t* sel_counts;  // [units]
+  int32_t sel_row;
+  int32_t sel_parts;
+  __half* sel_out;
+  int32_t out_half;       // the combine kernel writes fp16 (the flattened form of the same)
 };
 
 // ------------------------------------------------------------------ helpers
@@ -358,6 +366,29 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// Barrier of the cluster with release / acquire of shared memory writes.
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// 16 bytes at shared address a of the cluster's CTA `rank`.
+__device__ __forceinline__ float4 ld_cluster4(uint32_t a, int rank) {
+  uint32_t ra;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(ra));
+  return v;
+}
+
+// fp32 at shared address a of the cluster's CTA `rank`.
+__device__ __forceinline__ float ld_cluster(uint32_t a, int rank) {
+  uint32_t ra;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(ra) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(ra));
+  return v;
+}
+
 // ------------------------------------------------------------------ kernel 1
 // Shared-memory loads at 32-bit addresses with immediate offsets.  volatile:
 // they must stay after the mbarrier wait that publishes the stage.
@@ -512,15 +543,18 @@ struct ChunkDesc {
   int32_t unit, b, kvh, n_tok;
   uint32_t page_ok;  // bit i: page i of the chunk has a valid id (else masked)
   int32_t c;         // chunk index within its unit
-  int32_t nc;        // chunks of the unit
-  int32_t len;       // attended length of the sequence
+  int32_t nc;        // chunks of the unit (selected pages: the sequence's length)
+  int32_t len;       // attended length of the sequence (selected pages: listed pages)
 };
 
 // q1 fragments live in shared memory (one copy per CTA) for the variants
 // where they would take 32+ registers; elsewhere in registers.
 __host__ __device__ constexpr bool decode_qf_smem(int D, int GPAD) { return D == 256 || GPAD == 16; }
 
-template <int D, int GPAD>
+// SEL: the q1 fragments pass through shared memory in every variant (the warps
+// build them in shares), over the rotated query they are made of (the same
+// size), and the logit seeds come as a part per warp.
+template <int D, int GPAD, bool SEL = false>
 struct DecodeSmem {
   static constexpr int kFullOff = 0;                              // kMaxStages mbarriers
   static constexpr int kEmptyOff = kFullOff + 8 * kMaxStages;     // abort flag (+ spare)
@@ -528,9 +562,10 @@ struct DecodeSmem {
   static constexpr int kQOff = (kMLOff + kWarps * 2 * GPAD * 4 + 15) / 16 * 16;  // [GPAD][D]
   static constexpr int kQInvOff = kQOff + GPAD * D * 4;           // [GPAD]
   static constexpr int kKofsOff = kQInvOff + GPAD * 4;            // [D/32][GPAD] logit seeds
-  static constexpr int kQfOff = (kKofsOff + (D / 32) * GPAD * 4 + 15) / 16 * 16;  // [D/16][GPAD/4][32] uint2
+  static constexpr int kQEnd = (kKofsOff + (SEL ? kWarps : 1) * (D / 32) * GPAD * 4 + 15) / 16 * 16;
+  static constexpr int kQfOff = SEL ? kQOff : kQEnd;              // [D/16][GPAD/4][32] uint2
   static constexpr int kStageOff =
-      ((kQfOff + (decode_qf_smem(D, GPAD) ? (D / 16) * (GPAD / 4) * 256 : 0)) + 127) / 128 * 128;
+      ((kQEnd + (!SEL && decode_qf_smem(D, GPAD) ? (D / 16) * (GPAD / 4) * 256 : 0)) + 127) / 128 * 128;
 };
 
 // Resident CTAs per SM the register budget is sized for: the accumulators
@@ -544,7 +579,14 @@ __host__ __device__ constexpr int decode_min_blocks(int D, int GPAD) {
 // halves (PV n-tile = 4 heads x (hi, lo), like QK) -- needed when the value
 // scales are fp32, since p = 1 times an fp32 scale is not an fp16 value;
 // otherwise one fp16 value per head (PV n-tile = 8 heads).
-template <int D, int BLOCK, int GPAD, int SCALE, int NBIT, bool PSPLIT, bool PF = false>
+//
+// SEL: attention over selected pages.  One unit per cluster: its CTAs take the
+// unit's chunks in turn (CTA k of n: chunks k, k + n, ..., so the shares are
+// equal whatever the list's length and the first entries can be read before
+// it is known), and instead of partials in the workspace and a second kernel
+// the warps' states meet in shared memory, read across the cluster (see the
+// end of the kernel).
+template <int D, int BLOCK, int GPAD, int SCALE, int NBIT, bool PSPLIT, bool PF = false, bool SEL = false>
 __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
     decode_split_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ RotParams rp) {
   constexpr int NB = D / BLOCK;
@@ -562,17 +604,26 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
   constexpr int EQ = D >= 128 ? D / 32 : 4;  // query rotation layout
   constexpr int LQ = D / EQ;
   constexpr int GPWQ = 32 / LQ;
-  using SM = DecodeSmem<D, GPAD>;
+  using SM = DecodeSmem<D, GPAD, SEL>;
   using SDec = ScaleDec<NB, SCALE>;
   constexpr int BPT = SDec::BPT;
 
+  extern __shared__ __align__(128) uint8_t smem[];
+  if constexpr (SEL) {   // the barriers need nothing of the preceding kernel
+    if (threadIdx.x == 0) {
+      uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kFullOff);
+      for (int s = 0; s < p.stages; ++s) mbar_init(&bars[s], 1);
+      *reinterpret_cast<volatile uint32_t*>(smem + SM::kEmptyOff) = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
   // Launched as a programmatic dependent of the preceding kernel (the token
   // write, typically): everything up to here overlaps it, and nothing is
   // read before its writes are complete and visible.
   griddep_wait();
   // the combine kernel may launch now: it waits for this grid before reading
   griddep_launch_dependents();
-  extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31;
   const int wid = threadIdx.x >> 5;
   const int j = lane & 3, r = lane >> 2;
@@ -589,38 +640,106 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
   const uint32_t desc_off = p.stage_bytes - (uint32_t)sizeof(ChunkDesc);
 
   const int64_t cta = blockIdx.x;
-  const int64_t T = total_chunks(p, cta == 0 && wid == 0);
-  // W = min(CTAs, chunks): every CTA below W gets a non-empty range, so the
-  // CTAs holding a unit's chunks are consecutive (the combine walks them)
-  const int64_t W = T < p.ctas ? T : p.ctas;
-  if (cta >= W) return;  // uniform over the CTA
-  const int64_t c0 = cta * T / W, c1 = (cta + 1) * T / W;
-  const int64_t nch = c1 - c0;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
-    *abort_s = 0;
-    fence_mbar_init();
+  int64_t c0, nch;
+  // SEL: the unit, its count and its sequence's length.  None of them stays in a
+  // register through the loop: the chunk descriptors carry what a refill needs.
+  int sel_unit = 0, sel_b = 0, sel_kvh = 0, sel_n = 0, sel_part = 0;
+  int64_t sel_seq = 0;
+  int32_t first_entry = -1;
+  // SEL: the query rows of this warp's rounds of the rotation, EQ halves a lane
+  constexpr int QR = SEL ? (GPAD + kWarps * GPWQ - 1) / (kWarps * GPWQ) : 1;
+  uint4 sel_q[QR];
+  // SEL: entries of chunk c of a unit's list, lane i the i-th and lane 31 the
+  // one before the first (in bounds of the row, whatever the count)
+  auto entry_of = [&](int unit, int64_t c) {
+    const int64_t at = c * p.pages_per_chunk + (lane == 31 ? -1 : lane);
+    return (lane < p.pages_per_chunk || lane == 31) && at >= 0 && at < p.sel_row
+               ? p.sel_pages[(int64_t)unit * p.sel_row + at] : -1;
+  };
+  if constexpr (SEL) {
+    sel_unit = (int)(blockIdx.x / (unsigned)p.sel_parts);
+    sel_part = (int)(blockIdx.x - (unsigned)sel_unit * (unsigned)p.sel_parts);
+    sel_b = sel_unit / g.hkv;
+    sel_kvh = sel_unit - sel_b * g.hkv;
+    // everything the first copies and the query need, on its way at once
+    sel_n = p.sel_counts[sel_unit];
+    sel_seq = p.seq_lens[sel_b];
+    first_entry = entry_of(sel_unit, sel_part + wid * p.sel_parts);
+#pragma unroll
+    for (int k = 0; k < QR; ++k) {
+      const int gg = (k * kWarps + wid) * GPWQ + lane / LQ;
+      const __half* src = p.q + ((int64_t)sel_unit * p.G + (gg < p.G ? gg : 0)) * D + (lane % LQ) * EQ;
+      if constexpr (EQ == 8) sel_q[k] = *reinterpret_cast<const uint4*>(src);
+      else {
+        const uint2 v = *reinterpret_cast<const uint2*>(src);
+        sel_q[k] = make_uint4(v.x, v.y, 0, 0);
+      }
+    }
+    if (sel_seq < 0 || sel_seq > (int64_t)g.max_pages * g.page_size) {
+      if (threadIdx.x == 0 && sel_part == 0) set_status(p.status, KVQ3_DEV_BAD_LEN);
+      sel_seq = 0;
+    }
+    if (sel_n < 0 || sel_n > p.sel_row) {
+      if (threadIdx.x == 0 && sel_part == 0) set_status(p.status, KVQ3_DEV_BAD_LEN);
+      sel_n = 0;
+    }
+    if (sel_seq == 0) sel_n = 0;   // no token, or a length that was refused
+    const int nc = (sel_n + p.pages_per_chunk - 1) / p.pages_per_chunk;
+    c0 = sel_part;
+    nch = nc > sel_part ? (nc - sel_part + p.sel_parts - 1) / p.sel_parts : 0;
+  } else {
+    const int64_t T = total_chunks(p, cta == 0 && wid == 0);
+    // W = min(CTAs, chunks): every CTA below W gets a non-empty range, so the
+    // CTAs holding a unit's chunks are consecutive (the combine walks them)
+    const int64_t W = T < p.ctas ? T : p.ctas;
+    if (cta >= W) return;  // uniform over the CTA
+    c0 = cta * T / W;
+    nch = (cta + 1) * T / W - c0;
   }
-  __syncthreads();
+
+  if constexpr (!SEL) {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
+      *abort_s = 0;
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
 
   // ---- producer: chunk descriptor + bulk copies of its pages, issued by one
   // whole warp (lane i copies page i of the chunk): warp 0 fills the first
   // stages; afterwards the last warp to release a stage refills it
   const uint64_t pol = policy_evict_first();
-  auto issue = [&](const Cursor& c, int stage, int64_t len) {   // warp-collective
+  auto issue = [&](const Cursor& c, int stage, int64_t len, int32_t entry = -1) {   // warp-collective
     uint8_t* dst = stg + (size_t)stage * p.stage_bytes;
     // chunk c.c covers logical pages c.c*ppc .. of sequence c.b (32-bit: a
     // sequence holds fewer than 2^31 tokens)
     const int ppc = p.pages_per_chunk;
-    const int tok0 = (int)c.c * p.chunk_tokens;
-    const int n_tok = min(p.chunk_tokens, (int)len - tok0);
-    const int npg = n_tok == p.chunk_tokens ? ppc : (n_tok + g.page_size - 1) / g.page_size;
     const int lp = (int)c.c * ppc + lane;
+    int n_tok, npg;
     int64_t pg = -1;
     const int64_t row = p.pf_n > 0 ? p.pf_seq : c.b;   // prefill tiles all read one sequence
-    if (lane < npg)
-      pg = p.page_table ? (int64_t)p.page_table[row * g.max_pages + lp] : row * g.max_pages + lp;
+    if constexpr (SEL) {
+      // entry lp of the list: a page of the sequence above the entry before
+      // it, and whole unless it is the last
+      const int sel_n = (int)len;      // listed pages
+      const int64_t sel_seq = c.nc;    // the sequence's length
+      npg = min(ppc, sel_n - (int)c.c * ppc);
+      const int32_t before = __shfl_sync(kFull, entry, (lane + 31) & 31);
+      const int64_t e = entry, end = (e + 1) * g.page_size;
+      const bool last = lp == sel_n - 1;
+      if (lane < npg && e >= 0 && end - g.page_size < sel_seq && e > before && (end <= sel_seq || last))
+        pg = p.page_table ? (int64_t)p.page_table[row * g.max_pages + e] : row * g.max_pages + e;
+      // the last listed page counts up to the sequence's length
+      const int cut = lane < npg && last && e >= 0 && end > sel_seq && end - g.page_size < sel_seq ? (int)(end - sel_seq) : 0;
+      n_tok = npg * g.page_size - __shfl_sync(kFull, cut, npg - 1);
+    } else {
+      const int tok0 = (int)c.c * p.chunk_tokens;
+      n_tok = min(p.chunk_tokens, (int)len - tok0);
+      npg = n_tok == p.chunk_tokens ? ppc : (n_tok + g.page_size - 1) / g.page_size;
+      if (lane < npg)
+        pg = p.page_table ? (int64_t)p.page_table[row * g.max_pages + lp] : row * g.max_pages + lp;
+    }
     const bool ok = pg >= 0 && pg < g.num_pages;
     const uint32_t okm = __ballot_sync(kFull, ok);
     if (lane == 0) {
@@ -645,7 +764,15 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
       bulk_g2s(dst + (size_t)lane * 2 * REC, p.pool + (int64_t)(c.kvh * 2) * REC + pg * g.page_bytes, 2 * REC,
                &full[stage], pol);
   };
-  {
+  if constexpr (SEL) {
+    // each warp fills the stages wid, wid + 4, ..., its first entries read
+    // together with the count and the length
+    int32_t entry = first_entry;
+    for (int64_t i = wid; i < nch && i < S; i += kWarps) {
+      issue(Cursor{sel_b, sel_kvh, c0 + i * p.sel_parts, sel_seq}, (int)i, sel_n, entry);
+      entry = entry_of(sel_unit, c0 + (i + kWarps) * p.sel_parts);
+    }
+  } else {
     Cursor cp = cursor_at(p, c0);  // warp-collective
     if (wid == 0) {
       for (int64_t i = 0; i < nch && i < S; ++i) {
@@ -947,6 +1074,144 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
 #pragma unroll
       for (int b = 0; b < (ASYM ? NB : 1); ++b) zacc[tp][b] = 0.0f;
     named_barrier(1, 128);  // qs is rewritten at the next unit
+  };
+
+  // SEL: setup_unit for the CTA's one unit, from the query rows loaded at the
+  // start; the warps build the fragments in shares (k-steps wid, wid + 4, ...)
+  // and read them back from shared memory.
+  auto setup_sel = [&]() {
+#pragma unroll
+    for (int k = 0; k < QR; ++k) {
+      const int gg = (k * kWarps + wid) * GPWQ + gq;
+      const bool valid = gg < p.G;
+      const uint32_t w[4] = {sel_q[k].x, sel_q[k].y, sel_q[k].z, sel_q[k].w};
+      float x[EQ];
+#pragma unroll
+      for (int e = 0; e < EQ; e += 2) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[e / 2]));
+        x[e] = valid ? f.x : 0.0f;
+        x[e + 1] = valid ? f.y : 0.0f;
+      }
+      float4 quat_q[EQ / 4], quat_r[EQ / 4];
+      lane_quats<EQ>(rp, rq, quat_q);
+      lane_quats_r<EQ>(rp, rq, quat_r);
+      rotate_forward<EQ, LQ>(x, rq, sgn_q, quat_q, quat_r, p.inv_sqrt_d, rot_so4(rp), rot_pair(rp));
+      float amax = 0.0f;
+#pragma unroll
+      for (int e = 0; e < EQ; ++e) {
+        x[e] *= p.qk_scale;
+        amax = fmaxf(amax, fabsf(x[e]));
+      }
+#pragma unroll
+      for (int o = 1; o < LQ; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+      // 2^ex scales the largest magnitude into [2^7, 2^8): from its exponent
+      // bits; clamped, so that both powers stay normal
+      const int ea = (int)(__float_as_uint(amax) >> 23);   // 0 for zero and subnormals
+      const int ex = amax > 0.0f ? max(-100, min(100, 134 - ea)) : 8;
+      const float sc = __uint_as_float((uint32_t)(127 + ex) << 23);
+      if (gg < GPAD) {
+#pragma unroll
+        for (int e = 0; e < EQ; ++e) qs[gg * D + rq * EQ + e] = x[e] * sc;
+        if (rq == 0) qinv_s[gg] = __uint_as_float((uint32_t)(127 + 24 - ex) << 23);   // 2^24: subnormal key halves
+      }
+    }
+    named_barrier(1, 128);
+    // this warp's k-steps s = 4 i + wid (the field tables are compile-time in s:
+    // a switch on wid picks them)
+    constexpr int SW = KS / kWarps;
+    uint32_t q2[SW][NTQ][2];
+#pragma unroll
+    for (int tq = 0; tq < NTQ; ++tq) {
+      const int head = 4 * tq + (r >> 1);
+      const int part = r & 1;
+      float csum[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) csum[b] = 0.0f;
+      static_for<KS>([&](auto sc_) {
+        constexpr int s = decltype(sc_)::value;
+        constexpr int b = s / KSB, sp = s % KSB;
+        if (s % kWarps == wid) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const int P = 2 * sp + hf;
+            const int dlo = b * BLOCK + j * FQ + kp_fl(NBIT, FQ, P);
+            const int dhi = b * BLOCK + j * FQ + kp_fh(NBIT, FQ, P);
+            const float vlo = qs[head * D + dlo] * (1.0f / (float)(1 << kp_kl(NBIT, FQ, P)));
+            const float vhi = qs[head * D + dhi] * (1.0f / (float)(1 << kp_kh(NBIT, FQ, P)));
+            const __half hlo = __float2half_rn(vlo), hhi = __float2half_rn(vhi);
+            const float olo = part == 0 ? __half2float(hlo) : vlo - __half2float(hlo);
+            const float ohi = part == 0 ? __half2float(hhi) : vhi - __half2float(hhi);
+            const uint32_t w = pack_half2(olo, ohi);
+            q2[s / kWarps][tq][hf] = w;
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+            csum[b] += f.x * (float)(1 << kp_kl(NBIT, FQ, P)) + f.y * (float)(1 << kp_kh(NBIT, FQ, P));
+          }
+        }
+      });
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        float t = csum[b];
+        t += __shfl_xor_sync(kFull, t, 1);
+        t += __shfl_xor_sync(kFull, t, 2);
+        t += __shfl_xor_sync(kFull, t, 4);
+        if ((lane & 7) == 0) kofs_s[(wid * (D / 32) + b) * GPAD + 4 * tq + (lane >> 3)] = t;
+      }
+    }
+    named_barrier(1, 128);   // the fragments replace the rotated query
+#pragma unroll
+    for (int i = 0; i < SW; ++i)
+#pragma unroll
+      for (int tq = 0; tq < NTQ; ++tq)
+        qf_s[((i * kWarps + wid) * NTQ + tq) * 32 + lane] = make_uint2(q2[i][tq][0], q2[i][tq][1]);
+    named_barrier(1, 128);
+#pragma unroll
+    for (int tq = 0; tq < NTQ; ++tq) {
+      qinv[tq] = qinv_s[4 * tq + j];
+      m[tq] = -INFINITY;
+      l[tq] = 0.0f;
+    }
+    if constexpr (!QF_SMEM) {
+      // volatile loads: the fragments stay in registers (the compiler would
+      // otherwise read them again in every step)
+      static_for<KS * NTQ>([&](auto ic) {
+        constexpr int s = decltype(ic)::value / NTQ, tq = decltype(ic)::value % NTQ;
+        const uint2 v = lds64<(s * NTQ + tq) * 256>(qf_lane);
+        constexpr int t1 = QF_SMEM ? 0 : tq, s1 = QF_SMEM ? 0 : s;
+        qf[t1][s1][0] = v.x;
+        qf[t1][s1][1] = v.y;
+      });
+    }
+    // the seeds of setup_unit, the four warps' parts added in order
+    float seed[NB][NTQ];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int tq = 0; tq < NTQ; ++tq) {
+        float t = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) t += kofs_s[(w * (D / 32) + b) * GPAD + 4 * tq + j];
+        seed[b][tq] = (ASYM ? 1.0f : -(float)(1 << (NBIT - 1))) * 0x1p-24f * t;
+        if constexpr (KOFS_REG) kofs[b][tq] = seed[b][tq];
+      }
+    if constexpr (!KOFS_REG) {
+      named_barrier(1, 128);
+      if (wid == 0 && r == 0)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int tq = 0; tq < NTQ; ++tq) kofs_s[b * GPAD + 4 * tq + j] = seed[b][tq];
+      named_barrier(1, 128);
+    }
+#pragma unroll
+    for (int mt = 0; mt < KS; ++mt)
+#pragma unroll
+      for (int tp = 0; tp < NTP; ++tp)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[mt][tp][c] = 0.0f;
+#pragma unroll
+    for (int tp = 0; tp < (ASYM ? NTP : 1); ++tp)
+#pragma unroll
+      for (int b = 0; b < (ASYM ? NB : 1); ++b) zacc[tp][b] = 0.0f;
   };
 
   // A 16-token step at token offset t0 of a page whose K record starts at
@@ -1259,6 +1524,11 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
     });
   };
 
+  if constexpr (SEL) {
+    // while the first copies are in flight; the time-out path skips the unit's
+    // chunks but not the cluster's merge, so the state is set up in any case
+    setup_sel();
+  }
   const int P = g.page_size;
   int stage = 0;          // i mod S
   uint32_t parity = 0;    // (i / S) mod 2
@@ -1284,7 +1554,8 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
       const int64_t last = i == 0 ? (int64_t)S - 1 : i + S - 2;
       for (int64_t k = i; k < nch && k <= last; ++k)
         mbar_wait(&full[k % S], (uint32_t)((k / S) & 1), kDrainPolls);
-      return;
+      if constexpr (SEL) break;   // the cluster's other CTAs wait for this one's state
+      else return;
     }
     if (i > 0 && (((int)i - 1) & (kWarps - 1)) == wid && i - 1 + S < nch) {
       // chunk i - 1 + S; within the same sequence no global read is needed
@@ -1294,23 +1565,26 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
       const uint4 px = lds128<16>(sp + desc_off);     // page_ok, c, nc, len
       Cursor c{(int)pv.y, (int)pv.z, (int64_t)px.y, (int64_t)px.z};
       const int b_now = c.b;
-      for (int k = 0; k < S; ++k) cursor_next(p, c);
-      const int64_t len = c.b == b_now ? (int64_t)px.w : seq_len_checked(p, c.b, false);
+      if constexpr (SEL) c.c += (int64_t)S * p.sel_parts;
+      else
+        for (int k = 0; k < S; ++k) cursor_next(p, c);
+      const int64_t len = SEL || c.b == b_now ? (int64_t)px.w : seq_len_checked(p, c.b, false);
       fence_proxy_async();
-      issue(c, prev, len);
+      if constexpr (SEL) issue(c, prev, len, entry_of((int)pv.x, c.c));
+      else issue(c, prev, len);
     }
     const uint32_t st = stg_u32 + (uint32_t)stage * p.stage_bytes;
     const uint4 dv = lds128<0>(st + desc_off);            // unit, b, kvh, n_tok
     const uint2 dw = lds64<16>(st + desc_off);            // page_ok, c
     const int unit = (int)dv.x, n_tok = (int)dv.w;
     const uint32_t page_ok = dw.x;
-    if (unit != cur_unit) {
+    if (!SEL && unit != cur_unit) {
       if (cur_unit >= 0) flush(cur_unit, cur_first, cur_last);
       setup_unit((int)dv.y, (int)dv.z);
       cur_unit = unit;
       cur_first = dw.y == 0;
     }
-    cur_last = (int)dw.y == (int)lds32<24>(st + desc_off) - 1;   // c == nc - 1
+    if constexpr (!SEL) cur_last = (int)dw.y == (int)lds32<24>(st + desc_off) - 1;   // c == nc - 1
     if (!PF && n_tok == p.chunk_tokens && page_ok == (1u << p.pages_per_chunk) - 1u &&
         p.chunk_tokens % (16 * kWarps) == 0 &&
         KVQ3_CHECK(p.status, in_range(SM::kStageOff + (int64_t)stage * p.stage_bytes,
@@ -1384,7 +1658,140 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
       parity ^= 1u;
     }
   }
-  if (cur_unit >= 0) flush(cur_unit, cur_first, cur_last);
+  if constexpr (!SEL) {
+    if (cur_unit >= 0) flush(cur_unit, cur_first, cur_last);
+    return;
+  }
+  if constexpr (SEL) {
+    // Merge of the unit's warp states (4 per CTA of the cluster) and rotation
+    // back.  Every warp leaves its running maximum, sum and unnormalised
+    // output in its CTA's shared memory (the copy stages are free by now);
+    // after the cluster's barrier one warp per query head adds the states up
+    // in a fixed order, so the result does not depend on timing.
+    // A warp's output [GPAD heads][D] has a row of D + 16 floats: two of the
+    // eight lanes of a 16-byte store share a bank.
+    constexpr int OROW = D + 16;
+    float* part_s = reinterpret_cast<float*>(stg);   // [kWarps][GPAD][OROW]
+    named_barrier(1, 128);
+#pragma unroll
+    for (int tq = 0; tq < NTQ; ++tq) {
+      float lt = l[tq];
+      lt += __shfl_xor_sync(kFull, lt, 4);
+      lt += __shfl_xor_sync(kFull, lt, 8);
+      lt += __shfl_xor_sync(kFull, lt, 16);
+      if (r == 0) {
+        ml_s[(wid * 2 + 0) * GPAD + 4 * tq + j] = m[tq];
+        ml_s[(wid * 2 + 1) * GPAD + 4 * tq + j] = lt;
+      }
+    }
+    float zh[ASYM ? NTP : 1][ASYM ? NB : 1];
+    if constexpr (ASYM) {   // the zero-point sums of head 4tp + j (as in flush)
+#pragma unroll
+      for (int tp = 0; tp < NTP; ++tp)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float z = zacc[tp][b];
+          z += __shfl_xor_sync(kFull, z, 1);
+          z += __shfl_xor_sync(kFull, z, 2);
+          zh[tp][b] = __shfl_sync(kFull, z, 8 * j);
+        }
+    }
+    float* mine = part_s + wid * GPAD * OROW;
+#pragma unroll
+    for (int tp = 0; tp < NTP; ++tp) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        // this lane's fields f = 0 .. FV-1 of the block: dims b BLOCK + r FV + f
+#pragma unroll
+        for (int c = 0; c < (PSPLIT ? 1 : 2); ++c) {
+          float v[FV];
+#pragma unroll
+          for (int f = 0; f < FV; ++f) {
+            const float* a4 = acc[b * KSB + f / 2][tp];
+            const float sc = (float)(1 << (24 - v_off(NBIT, f)));   // value halves are c 2^(voff-24)
+            if constexpr (PSPLIT) {
+              v[f] = (a4[2 * (f % 2)] + a4[2 * (f % 2) + 1]) * sc;
+              if constexpr (ASYM) v[f] += zh[tp % (ASYM ? NTP : 1)][b % (ASYM ? NB : 1)];
+            } else {
+              v[f] = a4[2 * (f % 2) + c] * sc;
+            }
+          }
+          float* dst = mine + (PSPLIT ? 4 * tp + j : 8 * tp + 2 * j + c) * OROW + b * BLOCK + r * FV;
+#pragma unroll
+          for (int f = 0; f < FV; f += 4)
+            *reinterpret_cast<float4*>(dst + f) = make_float4(v[f], v[f + 1], v[f + 2], v[f + 3]);
+        }
+      }
+    }
+    cluster_sync_all();
+    const int parts = p.sel_parts, unit = (int)(blockIdx.x / (unsigned)parts);
+    const int rank = (int)(blockIdx.x - (unsigned)unit * (unsigned)parts);
+    const uint32_t sgn = lane_signs<EQ>(rp, rq);
+    const int ns = parts * kWarps;   // states of the unit: at most 64, two a lane
+    const uint32_t ml_a = smem_u32(ml_s), part_a = smem_u32(part_s);
+    for (int h = rank + parts * wid; h < p.G; h += parts * kWarps) {
+      float mv[2], lv[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = lane + 32 * k;
+        mv[k] = -INFINITY;
+        lv[k] = 0.0f;
+        if (i < ns) {
+          mv[k] = ld_cluster(ml_a + (uint32_t)(((i % kWarps) * 2 + 0) * GPAD + h) * 4u, i / kWarps);
+          lv[k] = ld_cluster(ml_a + (uint32_t)(((i % kWarps) * 2 + 1) * GPAD + h) * 4u, i / kWarps);
+        }
+      }
+      float M = fmaxf(mv[0], mv[1]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+      float wv[2], L = 0.0f;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        wv[k] = mv[k] == -INFINITY ? 0.0f : ex2(mv[k] - M);
+        L = fmaf(wv[k], lv[k], L);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(kFull, L, o);
+      const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+      float o1[EQ];
+#pragma unroll
+      for (int e = 0; e < EQ; ++e) o1[e] = 0.0f;
+      for (int i0 = 0; i0 < ns; i0 += kWarps) {   // a CTA's four states
+        float4 v[kWarps][EQ / 4];
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+#pragma unroll
+          for (int e = 0; e < EQ / 4; ++e)
+            v[w][e] = ld_cluster4(part_a + (uint32_t)((w * GPAD + h) * OROW + rq * EQ + 4 * e) * 4u, i0 / kWarps);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float c = __shfl_sync(kFull, i0 < 32 ? wv[0] : wv[1], (i0 + w) & 31);
+#pragma unroll
+          for (int e = 0; e < EQ / 4; ++e) {
+            o1[4 * e + 0] = fmaf(c, v[w][e].x, o1[4 * e + 0]);
+            o1[4 * e + 1] = fmaf(c, v[w][e].y, o1[4 * e + 1]);
+            o1[4 * e + 2] = fmaf(c, v[w][e].z, o1[4 * e + 2]);
+            o1[4 * e + 3] = fmaf(c, v[w][e].w, o1[4 * e + 3]);
+          }
+        }
+      }
+      float4 qt[EQ / 4], qtr[EQ / 4];
+      lane_quats<EQ>(rp, rq, qt);
+      lane_quats_r<EQ>(rp, rq, qtr);
+#pragma unroll
+      for (int e = 0; e < EQ; ++e) o1[e] *= inv;
+      rotate_inverse<EQ, LQ>(o1, rq, sgn, qt, qtr, p.inv_sqrt_d, rot_so4(rp), rot_pair(rp));
+      if (gq == 0) {
+        __half* dst = p.sel_out + ((int64_t)unit * p.G + h) * D + rq * EQ;
+#pragma unroll
+        for (int e = 0; e < EQ; e += 4)   // 8-byte aligned
+          *reinterpret_cast<uint2*>(dst + e) = make_uint2(pack_half2(o1[e], o1[e + 1]), pack_half2(o1[e + 2], o1[e + 3]));
+      }
+    }
+    // no CTA leaves while another reads its shared memory (the reads are done:
+    // their values went into the result)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+  }
 }
 
 // ------------------------------------------------------------------ kernel 2
@@ -1475,12 +1882,13 @@ struct DecodePlan {
   int chunk_tokens, pages_per_chunk;
   uint32_t stage_bytes, smem;
   size_t ws_bytes;
+  int clusters[9];   // SEL: resident clusters of 1..8 CTAs
 };
 
-template <int D, int BLOCK, int GPAD, int SCALE, int NBIT, bool PSPLIT, bool PF = false>
+template <int D, int BLOCK, int GPAD, int SCALE, int NBIT, bool PSPLIT, bool PF = false, bool SEL = false>
 kvq3_status decode_plan_t(const CacheGeom& g, int G, DecodePlan* plan) {
-  using SM = DecodeSmem<D, GPAD>;
-  const void* k = reinterpret_cast<const void*>(&decode_split_kernel<D, BLOCK, GPAD, SCALE, NBIT, PSPLIT, PF>);
+  using SM = DecodeSmem<D, GPAD, SEL>;
+  const void* k = reinterpret_cast<const void*>(&decode_split_kernel<D, BLOCK, GPAD, SCALE, NBIT, PSPLIT, PF, SEL>);
   plan->gpad = GPAD;
   // the SM's 228 KB of shared memory split over the CTAs that the register
   // budget lets reside (1 KB of it reserved per CTA)
@@ -1509,11 +1917,16 @@ kvq3_status decode_plan_t(const CacheGeom& g, int G, DecodePlan* plan) {
   // stages: as many as fit in the CTA's share; at least 2
   int stages = per_cta > SM::kStageOff ? (int)((per_cta - SM::kStageOff) / plan->stage_bytes) : 0;
   stages = stages < 2 ? 2 : (stages > kMaxStages ? kMaxStages : stages);
-  const size_t smem = SM::kStageOff + (size_t)stages * plan->stage_bytes;
+  size_t smem = SM::kStageOff + (size_t)stages * plan->stage_bytes;
+  if (SEL) {   // the warps' states of the merge lie over the stages
+    const size_t states = SM::kStageOff + (size_t)kWarps * GPAD * (D + 16) * sizeof(float);
+    smem = smem > states ? smem : states;
+  }
   if (smem > 227 * 1024) return KVQ3_ERR_UNSUPPORTED;  // pages too large for a two-stage ring
   plan->stages = stages;
   plan->smem = (uint32_t)smem;
-  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+  const int most_smem = SEL ? 227 * 1024 : (int)smem;
+  if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem) != cudaSuccess ||
       cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return KVQ3_ERR_CUDA;
   int per_sm = 0;
@@ -1565,6 +1978,72 @@ kvq3_status decode_run_t(const DecodePlan& plan, DecodeParams prm, const RotPara
   return cudaGetLastError() == cudaSuccess ? KVQ3_OK : KVQ3_ERR_CUDA;
 }
 
+// Launch of the SEL form: clusters of prm.sel_parts CTAs, one per unit.
+template <int D, int BLOCK, int GPAD, int SCALE, int NBIT, bool PSPLIT>
+kvq3_status pages_run_t(const DecodePlan& plan, DecodeParams prm, const RotParams& rp, cudaStream_t st) {
+  prm.stages = plan.stages;
+  prm.stage_bytes = plan.stage_bytes;
+  prm.chunk_tokens = plan.chunk_tokens;
+  prm.pages_per_chunk = plan.pages_per_chunk;
+  prm.smem_bytes = plan.smem;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)prm.sel_parts;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)prm.g.batch * prm.g.hkv * prm.sel_parts));
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = plan.smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, decode_split_kernel<D, BLOCK, GPAD, SCALE, NBIT, PSPLIT, false, true>, prm, rp) ==
+                 cudaSuccess
+             ? KVQ3_OK
+             : KVQ3_ERR_CUDA;
+}
+
+// The plan depends on the device and on the records' shape only; the last one
+// is kept by each host thread, since the occupancy queries cost more than the
+// launch.  The kernel's shared memory limit is set to the largest it may take,
+// so that threads with other shapes never lower it for one another.
+template <int D, int BLOCK, int GPAD, int SCALE, int NBIT, bool PSPLIT>
+kvq3_status pages_plan_t(const CacheGeom& g, int G, DecodePlan* plan) {
+  struct Kept {
+    int dev = -1;
+    int32_t page_size = 0;
+    DecodePlan plan;
+  };
+  static thread_local Kept kept;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return KVQ3_ERR_CUDA;
+  if (kept.dev != dev || kept.page_size != g.page_size) {   // D, BLOCK, SCALE and NBIT fix the rest of a record
+    kept.dev = -1;
+    const kvq3_status s = decode_plan_t<D, BLOCK, GPAD, SCALE, NBIT, PSPLIT, false, true>(g, G, &kept.plan);
+    if (s != KVQ3_OK) return s;
+    auto* k = &decode_split_kernel<D, BLOCK, GPAD, SCALE, NBIT, PSPLIT, false, true>;
+    for (int n = 1; n <= 8; ++n) {
+      cudaLaunchAttribute attr[1];
+      attr[0].id = cudaLaunchAttributeClusterDimension;
+      attr[0].val.clusterDim.x = (unsigned)n;
+      attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)n);
+      cfg.blockDim = dim3(32 * kWarps);
+      cfg.dynamicSmemBytes = kept.plan.smem;
+      cfg.attrs = attr;
+      cfg.numAttrs = 1;
+      if (cudaOccupancyMaxActiveClusters(&kept.plan.clusters[n], k, &cfg) != cudaSuccess) return KVQ3_ERR_CUDA;
+    }
+    kept.dev = dev;
+    kept.page_size = g.page_size;
+  }
+  *plan = kept.plan;
+  return KVQ3_OK;
+}
+
 // Per-(head dim, scale type, code width) entry points, one translation unit each.
 #define KVQ3_DECODE_DECL1(D, SN, NB)                                                          \
   kvq3_status decode_plan_d##D##_##SN##_b##NB(const CacheGeom& g, int G, DecodePlan* plan);  \
@@ -1572,7 +2051,10 @@ kvq3_status decode_run_t(const DecodePlan& plan, DecodeParams prm, const RotPara
                                              const RotParams&, float*, cudaStream_t);         \
   kvq3_status prefill_plan_d##D##_##SN##_b##NB(const CacheGeom& g, int G, DecodePlan* plan); \
   kvq3_status prefill_run_d##D##_##SN##_b##NB(const DecodePlan&, const DecodeParams&,         \
-                                              const RotParams&, float*, cudaStream_t);
+                                              const RotParams&, float*, cudaStream_t);        \
+  kvq3_status pages_plan_d##D##_##SN##_b##NB(const CacheGeom& g, int G, DecodePlan* plan);   \
+  kvq3_status pages_run_d##D##_##SN##_b##NB(const DecodePlan&, const DecodeParams&,           \
+                                            const RotParams&, cudaStream_t);
 #define KVQ3_DECODE_DECL(D, SN) KVQ3_DECODE_DECL1(D, SN, 2) KVQ3_DECODE_DECL1(D, SN, 3) KVQ3_DECODE_DECL1(D, SN, 4)
 KVQ3_DECODE_DECL(64, f32) KVQ3_DECODE_DECL(64, f16) KVQ3_DECODE_DECL(64, e4m3)
 KVQ3_DECODE_DECL(128, f32) KVQ3_DECODE_DECL(128, f16) KVQ3_DECODE_DECL(128, e4m3)
@@ -1614,6 +2096,17 @@ KVQ3_DECODE_DECL1(64, e4m3zp, 3) KVQ3_DECODE_DECL1(128, e4m3zp, 3) KVQ3_DECODE_D
                                               const RotParams& rp, float* out, cudaStream_t st) { \
     if (prm.g.block == 32) return decode_run_t<D, 32, 8, SC, NB, true, true>(plan, prm, rp, out, st); \
     return decode_run_t<D, 64, 8, SC, NB, true, true>(plan, prm, rp, out, st);                \
+  }                                                                                           \
+  kvq3_status pages_plan_d##D##_##SN##_b##NB(const CacheGeom& g, int G, DecodePlan* plan) {  \
+    const int gp = G <= 4 ? 4 : (G <= 8 ? 8 : 16);                                            \
+    if (g.block == 32) KVQ3_DECODE_PICK(D, 32, SC, NB, pages_plan_t, g, G, plan)              \
+    KVQ3_DECODE_PICK(D, 64, SC, NB, pages_plan_t, g, G, plan)                                 \
+  }                                                                                           \
+  kvq3_status pages_run_d##D##_##SN##_b##NB(const DecodePlan& plan, const DecodeParams& prm,  \
+                                            const RotParams& rp, cudaStream_t st) {           \
+    const int gp = plan.gpad;                                                                 \
+    if (prm.g.block == 32) KVQ3_DECODE_PICK(D, 32, SC, NB, pages_run_t, plan, prm, rp, st)    \
+    KVQ3_DECODE_PICK(D, 64, SC, NB, pages_run_t, plan, prm, rp, st)                           \
   }
 
 }  // namespace kvq3

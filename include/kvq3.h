@@ -514,7 +514,7 @@ kvq3_status kvq3_decode_pages_workspace_size(const kvq3_cache_desc *desc, int32_
  * (KVQ3_DEV_BAD_LEN), and so does an empty list.
  * q: device fp16 [batch][Hq][d]; out: device fp16 [batch][Hq][d], what the
  * projection after it reads (one rounding of the fp32 result, 2^-11 relative,
- * below the error bar of the attention).  workspace: device, 256-byte
+ * below the error bar of the attention); both 16-byte aligned.  workspace: device, 256-byte
  * aligned, ws_bytes >= kvq3_decode_pages_workspace_size; calls sharing it must
  * not overlap.  The rest as for kvq3_decode_attn; KVQ3_ERR_UNSUPPORTED when
  * num_pages * Hkv, batch * Hq or max_selected * P reaches 2^31. */

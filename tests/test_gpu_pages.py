@@ -315,6 +315,12 @@ ATTN = [
     (dict(lens=(333, 20, 64), scale="e4m3zp", paged=False), 4, 4),
     (dict(lens=(5000, 4999, 3), page=16, hkv=8), 4, 200),
     (dict(lens=tuple(5 + 7 * i for i in range(70)), page=16, hkv=4), 4, 4),   # many short units
+    # few units with long lists: the flattened form
+    (dict(lens=(40000,), page=16, hkv=1), 4, 2600),
+    (dict(lens=(60000, 300), page=64, hkv=1, scale="e4m3", flags=7), 8, 800),
+    (dict(lens=(33000, 0, 17), page=16, hkv=1, scale="e4m3zp", d=64, block=32), 3, 2000),
+    # long lists of several units: whole clusters, chunks in turn
+    (dict(lens=(9000, 8000, 100, 0), page=32, hkv=4, bits=4), 6, 250),
 ]
 
 
@@ -341,17 +347,18 @@ def test_all_pages_is_the_dense_decode():
     _near(got, out.cpu().numpy().astype(np.float64))
 
 
-def test_decode_attn_pages_bad_lists():
+@pytest.mark.parametrize("row", [5, 40000])   # the cluster form, and (long lists of few units) the flattened one
+def test_decode_attn_pages_bad_lists(row):
     c = Pages(lens=(100, 100, 100, 100, 100, 50), hkv=1, page=16, maxp=8)
     q = c.queries(4)
-    pages = np.full((6, 1, 5), -1, np.int32)
-    pages[0, 0] = [0, 2, 2, 5, 6]            # a page twice
-    pages[1, 0] = [1, 6, 3, 7, -2]           # not ascending; the part-filled page before the end; past the end
-    pages[2, 0] = [6, 6, 6, 6, 6]            # the part-filled page again
-    pages[3, 0] = [0, 1, 2, 3, 4]
-    pages[4, 0] = [0, 1, 2, 1 << 30, 3]
-    pages[5, 0] = [0, 1, 2, 3, 4]
-    counts = np.array([[5], [5], [5], [6], [5], [2]], np.int32)   # row 3: more than the list holds
+    pages = np.full((6, 1, row), -1, np.int32)
+    pages[0, 0, :5] = [0, 2, 2, 5, 6]            # a page twice
+    pages[1, 0, :5] = [1, 6, 3, 7, -2]           # not ascending; the part-filled page before the end; past the end
+    pages[2, 0, :5] = [6, 6, 6, 6, 6]            # the part-filled page again
+    pages[3, 0, :5] = [0, 1, 2, 3, 4]
+    pages[4, 0, :5] = [0, 1, 2, 1 << 30, 3]
+    pages[5, 0, :5] = [0, 1, 2, 3, 4]
+    counts = np.array([[5], [5], [5], [row + 1], [5], [2]], np.int32)   # row 3: more than the list holds
     c.table[5, 1] = c.N + 4
     c.table_t.copy_(c.dev(c.table))
     want = PO.decode_pages(c.pool, c.layout, c.U, q, c.lens, c.table, pages, counts)
@@ -363,6 +370,41 @@ def test_decode_attn_pages_bad_lists():
     c.lens = np.array([100, -1, 129, 100, 100, 50], np.int32)
     want = PO.decode_pages(c.pool, c.layout, c.U, q, c.lens, c.table, pages, counts)
     _near(_attend(c, q, pages, counts), want)
+
+
+@pytest.mark.parametrize("kw,G,row", [
+    (dict(lens=(700, 1, 129, 64), page=64), 4, 9), (dict(lens=(300, 17, 1000), d=256, page=16), 4, 70),
+    (dict(lens=(40000,), page=16, hkv=1), 4, 2600)])
+def test_decode_attn_pages_wait_that_runs_out(kw, G, row):
+    # with no poll allowed every CTA takes its time-out path: it flags, drains its copies and still meets the
+    # others of its cluster; a normal call on the same buffers follows
+    import ctypes
+    c = Pages(**kw)
+    K, t = c.K, c.torch
+    fn = K.lib.kvq3_test_decode_pages_polls
+    fn.restype, fn.argtypes = ctypes.c_int, K.lib.kvq3_decode_attn_pages.argtypes + [ctypes.c_uint32]
+    q = c.queries(G)
+    pages, counts = _lists(c, row)
+    qd, pd, nd = c.dev(q), c.dev(pages), c.dev(counts)
+    out = t.empty(q.shape, dtype=t.float16, device="cuda")
+    ws = t.empty(K.kvq3_decode_pages_workspace_size(c.desc, q.shape[1], row), dtype=t.uint8, device="cuda")
+    for _ in range(2):
+        assert fn(c.rot.handle, c.desc, c.cache, qd.data_ptr(), q.shape[1], 0.0, pd.data_ptr(), nd.data_ptr(), row,
+                  out.data_ptr(), ws.data_ptr(), ws.numel(), c.status.data_ptr(), K._raw_stream(None), 0) == 0
+        t.cuda.synchronize()
+        assert c.flags() & K.DEV_BITS["timeout"]
+        c.status.zero_()
+    _near(_attend(c, q, pages, counts), PO.decode_pages(c.pool, c.layout, c.U, q, c.lens, c.table, pages, counts))
+    assert c.flags() == 0
+
+
+def test_decode_attn_pages_is_deterministic():
+    c = Pages(lens=(5000, 4000, 77), page=16, hkv=4)
+    q = c.queries(4)
+    pages, counts = _lists(c, 250)
+    first = _attend(c, q, pages, counts)
+    for _ in range(5):
+        assert np.array_equal(first, _attend(c, q, pages, counts))
 
 
 # ------------------------------------------------------------ remapping

@@ -73,7 +73,8 @@ def test_decode_attn_pages_refusals(K):
         return K.lib.kvq3_decode_attn_pages(r, ctypes.byref(desc or _desc(K)), ctypes.byref(cache or _cache(K)), q, hq, sm,
                                             pages, counts, n, out, None, 0, None, None)
     for kw in (dict(r=None), dict(r=rot64.handle), dict(q=None), dict(pages=None), dict(counts=None), dict(out=None),
-               dict(hq=0), dict(hq=9), dict(n=0), dict(n=-3), dict(sm=float("inf")), dict(cache=_cache(K, lens=None))):
+               dict(hq=0), dict(hq=9), dict(n=0), dict(n=-3), dict(sm=float("inf")), dict(cache=_cache(K, lens=None)),
+               dict(q=ctypes.c_void_p(4104)), dict(out=ctypes.c_void_p(4098))):
         assert call(**kw) == INVALID, kw
     assert call(hq=34) == UNSUPPORTED
     assert call(n=(1 << 31) // 16) == UNSUPPORTED                               # a list of 2^31 tokens
