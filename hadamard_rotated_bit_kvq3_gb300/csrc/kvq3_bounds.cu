@@ -24,7 +24,11 @@ using namespace kvq3;
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
+#ifndef KLT
+#define KLT 32
+#endif
+constexpr int kLaneTokens = KLT;
 constexpr int kSeg = 1024;   // sequences whose page counts are held in shared memory at a time
 
 // Page count of every sequence of a segment as an inclusive running sum in
@@ -292,9 +296,12 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     const int64_t pages = segment_pages(g, seq_lens, first, b0, psum, pfirst, status, blockIdx.x == 0);
     const int64_t units = pages * g.hkv;
-    // lanes that share a page's tokens: more of them while the GPU is not full
+    // lanes that share a page's tokens: two more while the GPU is not full, or
+    // while its last round would idle and each keeps kLaneTokens tokens
     int sub = 1;
-    while (sub * ng < 32 && units * ng * sub < nthreads / 2) sub <<= 1;
+    while (sub * ng < 32 && (units * ng * sub < nthreads / 2 ||
+                             (units * ng * sub < 8 * nthreads && g.page_size >= 2 * sub * kLaneTokens)))
+      sub <<= 1;
     const int per = ng * sub;                 // lanes of a unit
     const int64_t lanes = (units * per + 31) / 32 * 32;   // whole warps: shuffles below
     for (int64_t i = thread; i < lanes; i += nthreads) {
@@ -323,20 +330,30 @@ __global__ void __launch_bounds__(kThreads)
         const uint8_t* codes = rec + g.scale_hdr_bytes + grp * (4 * NBIT);
         const uint8_t* scales = rec + (grp * 32 / g.block) * g.sb;
         const int tb = g.nb * g.sb;
+        // U tokens at a time, the next U on their way meanwhile; a token index
+        // past the last is clamped to it (minima and maxima do not mind a
+        // token twice)
         constexpr int U = 4;
-        // a token index past the last is clamped to it: minima and maxima do
-        // not mind a token twice
-        for (int t0 = s; t0 < n; t0 += U * sub) {
-          Codes<NBIT> c[U];
-          uint32_t sc[U];
+        Codes<NBIT> c[U], cn[U];
+        uint32_t sc[U], scn[U];
+        auto load = [&](int t0, Codes<NBIT>(&cc)[U], uint32_t(&ss)[U]) {
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const int t = min(t0 + u * sub, n - 1);
-            c[u] = load_codes<NBIT>(codes + t * g.cb);
-            sc[u] = load_scale<SCALE>(scales + t * tb);
+            cc[u] = load_codes<NBIT>(codes + (uint32_t)(t * g.cb));
+            ss[u] = load_scale<SCALE>(scales + (uint32_t)(t * tb));
           }
+        };
+        load(s, c, sc);
+        for (int t0 = s; t0 < n; t0 += U * sub) {
+          if (t0 + U * sub < n) load(t0 + U * sub, cn, scn);
 #pragma unroll
           for (int u = 0; u < U; ++u) acc.add(c[u], sc[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            c[u] = cn[u];
+            sc[u] = scn[u];
+          }
         }
       }
       for (int m = ng; m < per; m <<= 1) acc.meet(m);

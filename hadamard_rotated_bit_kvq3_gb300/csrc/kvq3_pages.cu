@@ -11,9 +11,11 @@
 // free pages a rank over a bitmap).
 //
 // The bookkeeping is a chain of dependent passes over the table and the page
-// bitmap (a few hundred KB at most), bound by the latency of its barriers: one
-// thread-block cluster runs all of them with the hardware cluster barrier
-// between, in one launch.  The copies of part-filled pages are the only bulk
+// bitmap (a few hundred KB at most), bound by the latency of its loads and
+// barriers.  A small table (up to 512 rows and 64K entries) is one CTA's work,
+// with the rows' state and the bitmap in shared memory and block barriers
+// between the passes; a larger one is a thread-block cluster's, its state in
+// the workspace and the hardware cluster barrier between, in one launch.  The copies of part-filled pages are the only bulk
 // traffic; a second kernel, launched as its programmatic dependent, spreads
 // them over the GPU and moves only the slots in use.
 //
@@ -34,6 +36,12 @@ namespace {
 
 constexpr int kMapThreads = 1024;
 constexpr int kMapCluster = 8;      // CTAs of the remap cluster (the portable maximum)
+// What one CTA takes: a cluster barrier costs over a microsecond with the
+// workspace's writes in flight, a block barrier almost nothing, but one SM
+// moves only about 100 GB/s of table.
+constexpr int kSmallRows = 512;
+constexpr int kSmallEntries = 65536;
+constexpr int kSmallPages = 131072;
 
 // What the remap keeps in its workspace.
 struct RemapWs {
@@ -92,16 +100,32 @@ __device__ __forceinline__ int64_t cta_excl(int64_t v, int64_t* wsum, int64_t* t
   return base + incl - v;
 }
 
+template <bool SMALL>
 __global__ void __launch_bounds__(kMapThreads)
     remap_kernel(const __grid_constant__ CacheGeom g, const int32_t* table, const int32_t* seq_lens, const int32_t* src,
-                 const int32_t* new_lens, int32_t* table_out, int32_t* lens_out, const __grid_constant__ RemapWs ws,
+                 const int32_t* new_lens, int32_t* table_out, int32_t* lens_out, const __grid_constant__ RemapWs global,
                  int32_t* status) {
   __shared__ int64_t wsum[kMapThreads / 32];
   __shared__ int64_t part[2];   // this CTA's free pages and wanted entries
+  __shared__ uint32_t bits_s[SMALL ? kSmallPages / 32 : 1];
+  __shared__ int64_t first_s[SMALL ? kSmallRows : 1];
+  __shared__ int4 rows_s[SMALL ? kSmallRows : 1];
+  __shared__ int32_t need_s[SMALL ? kSmallRows : 1], tail_s[SMALL ? kSmallRows : 1];
+  RemapWs ws = global;
+  if constexpr (SMALL) {
+    ws.bits = bits_s;
+    ws.first = first_s;
+    ws.rows = rows_s;
+    ws.need = need_s;
+    ws.tail = tail_s;
+  }
   griddep_wait();
   griddep_launch_dependents();
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ncta = (int)cluster.num_blocks();
+  const int rank = SMALL ? 0 : (int)cg::this_cluster().block_rank(), ncta = SMALL ? 1 : (int)cg::this_cluster().num_blocks();
+  auto sync = [] {
+    if constexpr (SMALL) __syncthreads();
+    else cg::this_cluster().sync();
+  };
   const int t = threadIdx.x, lane = t & 31;
   const int64_t th = (int64_t)rank * kMapThreads + t, nth = (int64_t)ncta * kMapThreads;
   const int64_t wp = th >> 5, nwp = nth >> 5;
@@ -141,7 +165,7 @@ __global__ void __launch_bounds__(kMapThreads)
     ws.copies[b] = make_int4(0, 0, 0, 0);
     lens_out[b] = (int32_t)held;
   }
-  cluster.sync();
+  sync();
   // whole pages are shared as they are
   for (int64_t b = wp; b < g.batch; b += nwp) {
     const int4 r = ws.rows[b];
@@ -159,18 +183,18 @@ __global__ void __launch_bounds__(kMapThreads)
       table_out[b * g.max_pages + i] = page;
     }
   }
-  cluster.sync();
+  sync();
   // owners of part-filled pages
   for (int64_t b = th; b < g.batch; b += nth) {
     const int tail = ws.tail[b];
     if (tail >= 0) atomicMin(&ws.owner[tail], (int32_t)b);
   }
-  cluster.sync();
+  sync();
   for (int64_t b = th; b < g.batch; b += nth) {
     const int4 r = ws.rows[b];
     const int tail = ws.tail[b];
     int keeps = 0;
-    if (tail >= 0 && ws.owner[tail] == b) {
+    if (tail >= 0 && __ldcg(&ws.owner[tail]) == b) {
       // only the owner may set this bit here, so it is clear unless some row shares the page whole
       const uint32_t bit = 1u << (tail & 31);
       if ((atomicOr(&ws.bits[tail >> 5], bit) & bit) == 0) {
@@ -183,12 +207,12 @@ __global__ void __launch_bounds__(kMapThreads)
     const int lost = r.z && tail < 0;
     ws.need[b] = r.w - r.y - (keeps | lost);
   }
-  cluster.sync();
+  sync();
   // ranks: every CTA counts the free pages and the wanted entries of its slice
   const int64_t w0 = words * rank / ncta, w1 = words * (rank + 1) / ncta;
   const int64_t b0 = (int64_t)g.batch * rank / ncta, b1 = (int64_t)g.batch * (rank + 1) / ncta;
   auto free_of = [&](int64_t w) {
-    uint32_t f = ~__ldcg(&ws.bits[w]);
+    uint32_t f = ~*const_cast<volatile uint32_t*>(&ws.bits[w]);
     if (w == words - 1 && (g.num_pages & 31)) f &= (1u << (g.num_pages & 31)) - 1u;
     return f;
   };
@@ -201,10 +225,10 @@ __global__ void __launch_bounds__(kMapThreads)
     cta_excl(n, wsum, &total);
     if (t == 0) part[1] = total;
   }
-  cluster.sync();
+  sync();
   int64_t free_before = 0, want_before = 0, free_all = 0, want_all = 0;
   for (int c = 0; c < ncta; ++c) {
-    const int64_t* other = cluster.map_shared_rank(part, c);
+    const int64_t* other = SMALL ? part : cg::this_cluster().map_shared_rank(part, c);
     const int64_t f = other[0], n = other[1];
     if (c < rank) {
       free_before += f;
@@ -234,7 +258,7 @@ __global__ void __launch_bounds__(kMapThreads)
     if (b < b1) ws.first[b] = at;
     want_before += total;
   }
-  cluster.sync();   // also: no CTA leaves while another reads its shared memory
+  sync();   // also: no CTA leaves while another reads its shared memory
   if (!enough) return;
   for (int64_t b = wp; b < g.batch; b += nwp) {
     const int4 r = ws.rows[b];
@@ -279,11 +303,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // ------------------------------------------------------------ compaction
-constexpr int kKeepTile = 256;   // kept tokens per CTA
+constexpr int kKeepTile = 128;   // kept tokens per CTA, one per thread
 
-// CV: bytes of a code access (16 or 8, dividing a code string); HV: bytes of a
-// header access (dividing a token's scales).
-template <typename CV, typename HV>
+// CV: a code access (16 or 8 bytes), CN of them in a code string; HV: a header
+// access, dividing a token's scales.
+template <typename CV, int CN, typename HV, int HN>
 __global__ void __launch_bounds__(kKeepTile)
     compact_kernel(const __grid_constant__ CacheGeom g, uint8_t* pool, const int32_t* __restrict__ page_table,
                    const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ src_seq,
@@ -298,6 +322,8 @@ __global__ void __launch_bounds__(kKeepTile)
   const int tile = (int)(blockIdx.x - unit * tiles);
   const int i = (int)(unit / g.hkv), kvh = (int)(unit - (int64_t)i * g.hkv);
   const int64_t cap = (int64_t)g.max_pages * g.page_size;
+  const int64_t at = (int64_t)tile * kKeepTile + t;
+  const int64_t pos = at < keep_stride ? keep[unit * keep_stride + at] : -1;   // with the pair's ids and count
   const int s = src_seq[i], d = dst_seq[i], n = n_keep[i];
   int bad = 0;
   int64_t len = 0;
@@ -310,84 +336,118 @@ __global__ void __launch_bounds__(kKeepTile)
     if (t == 0) set_status(status, bad);
     return;
   }
-  const int64_t t0 = (int64_t)tile * kKeepTile;
-  const int m = (int)min((int64_t)kKeepTile, n - t0);
+  const int m = (int)min((int64_t)kKeepTile, n - (int64_t)tile * kKeepTile);
   if (m <= 0) return;
+  int64_t a = -1, z = -1;
   if (t < m) {
-    const int64_t at = t0 + t;
-    const int64_t pos = keep[unit * keep_stride + at];
-    int64_t a = -1, z = -1;
     if (pos < 0 || pos >= len) {
       set_status(status, KVQ3_DEV_BAD_POS);
-    } else {
-      const int64_t ps = page_of(g, page_table, s, pos / g.page_size), pd = page_of(g, page_table, d, at / g.page_size);
+    } else {   // 32-bit positions: below 2^31
+      const uint32_t P = (uint32_t)g.page_size;
+      const uint32_t lp = (uint32_t)pos / P, ld = (uint32_t)at / P;
+      const int64_t ps = page_of(g, page_table, s, lp), pd = page_of(g, page_table, d, ld);
       if (ps < 0 || pd < 0) set_status(status, KVQ3_DEV_BAD_PAGE);
       else {
         a = record_offset(g, ps, kvh, 0);
         z = record_offset(g, pd, kvh, 0);
-        slots_s[t] = (int32_t)(pos % g.page_size) | ((int32_t)(at % g.page_size) << 16);
+        slots_s[t] = (int32_t)((uint32_t)pos - lp * P) | ((int32_t)((uint32_t)at - ld * P) << 16);
         if (!KVQ3_CHECK(status, in_range(a, 2 * g.record_bytes, g.num_pages * g.page_bytes) &&
                                     in_range(z, 2 * g.record_bytes, g.num_pages * g.page_bytes)))
           a = -1;
       }
     }
-    from_s[t] = a;
-    to_s[t] = z;
   }
+  from_s[t] = a;
+  to_s[t] = z;
   __syncthreads();
-  const int hb = g.nb * g.sb;
-  const int cn = g.cb / (int)sizeof(CV), hn = hb / (int)sizeof(HV);
+  // consecutive threads move consecutive pieces of a code string; every load
+  // of the thread is under way before its first store
+  CV c[2][CN];
+  HV h[2][HN];
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const int64_t rec = which * g.record_bytes;
-    for (int k = t; k < m * cn; k += kKeepTile) {
-      const int tok = k / cn, e = k - tok * cn;
-      const int64_t a = from_s[tok];
-      if (a < 0) continue;
-      const int sl = slots_s[tok];
-      reinterpret_cast<CV*>(pool + to_s[tok] + rec + g.scale_hdr_bytes + (int64_t)(sl >> 16) * g.cb)[e] =
-          reinterpret_cast<const CV*>(pool + a + rec + g.scale_hdr_bytes + (int64_t)(sl & 0xffff) * g.cb)[e];
-    }
-    for (int k = t; k < m * hn; k += kKeepTile) {
-      const int tok = k / hn, e = k - tok * hn;
-      const int64_t a = from_s[tok];
-      if (a < 0) continue;
-      const int sl = slots_s[tok];
-      reinterpret_cast<HV*>(pool + to_s[tok] + rec + (int64_t)(sl >> 16) * hb)[e] =
-          reinterpret_cast<const HV*>(pool + a + rec + (int64_t)(sl & 0xffff) * hb)[e];
-    }
+  for (int k = 0; k < CN; ++k) {
+    const int x = k * kKeepTile + t, tok = x / CN, e = x - tok * CN;
+    const int64_t f = from_s[tok];
+    if (f < 0) continue;
+    const uint8_t* p = pool + f + g.scale_hdr_bytes + (slots_s[tok] & 0xffff) * g.cb;
+    c[0][k] = reinterpret_cast<const CV*>(p)[e];
+    c[1][k] = reinterpret_cast<const CV*>(p + g.record_bytes)[e];
+  }
+#pragma unroll
+  for (int k = 0; k < HN; ++k) {
+    const int x = k * kKeepTile + t, tok = x / HN, e = x - tok * HN;
+    const int64_t f = from_s[tok];
+    if (f < 0) continue;
+    const uint8_t* p = pool + f + (slots_s[tok] & 0xffff) * (HN * (int)sizeof(HV));
+    h[0][k] = reinterpret_cast<const HV*>(p)[e];
+    h[1][k] = reinterpret_cast<const HV*>(p + g.record_bytes)[e];
+  }
+#pragma unroll
+  for (int k = 0; k < CN; ++k) {
+    const int x = k * kKeepTile + t, tok = x / CN, e = x - tok * CN;
+    if (from_s[tok] < 0) continue;
+    uint8_t* p = pool + to_s[tok] + g.scale_hdr_bytes + (slots_s[tok] >> 16) * g.cb;
+    reinterpret_cast<CV*>(p)[e] = c[0][k];
+    reinterpret_cast<CV*>(p + g.record_bytes)[e] = c[1][k];
+  }
+#pragma unroll
+  for (int k = 0; k < HN; ++k) {
+    const int x = k * kKeepTile + t, tok = x / HN, e = x - tok * HN;
+    if (from_s[tok] < 0) continue;
+    uint8_t* p = pool + to_s[tok] + (slots_s[tok] >> 16) * (HN * (int)sizeof(HV));
+    reinterpret_cast<HV*>(p)[e] = h[0][k];
+    reinterpret_cast<HV*>(p + g.record_bytes)[e] = h[1][k];
   }
 }
 
-template <typename CV, typename HV>
-cudaError_t launch_compact(const CacheGeom& g, const kvq3_cache* c, const int32_t* src_seq, const int32_t* dst_seq,
-                           int64_t units, const int32_t* keep, const int32_t* n_keep, int keep_stride, int32_t* st,
-                           cudaStream_t stream) {
-  const int tiles = (int)(((int64_t)keep_stride + kKeepTile - 1) / kKeepTile);
+struct CompactArgs {
+  const kvq3_cache* cache;
+  const int32_t *src_seq, *dst_seq, *keep, *n_keep;
+  int64_t units;
+  int keep_stride;
+  int32_t* status;
+  cudaStream_t stream;
+};
+
+template <typename CV, int CN, typename HV, int HN>
+cudaError_t launch_compact(const CacheGeom& g, const CompactArgs& a) {
+  const int tiles = (int)(((int64_t)a.keep_stride + kKeepTile - 1) / kKeepTile);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * tiles));
+  cfg.gridDim = dim3((unsigned)(a.units * tiles));
   cfg.blockDim = dim3(kKeepTile);
-  cfg.stream = stream;
+  cfg.stream = a.stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, compact_kernel<CV, HV>, g, static_cast<uint8_t*>(c->pool), c->page_table, c->seq_lens,
-                            src_seq, dst_seq, keep, n_keep, keep_stride, tiles, st);
+  return cudaLaunchKernelEx(&cfg, compact_kernel<CV, CN, HV, HN>, g, static_cast<uint8_t*>(a.cache->pool),
+                            a.cache->page_table, a.cache->seq_lens, a.src_seq, a.dst_seq, a.keep, a.n_keep,
+                            a.keep_stride, tiles, a.status);
 }
 
-template <typename CV>
-cudaError_t compact_by_header(const CacheGeom& g, const kvq3_cache* c, const int32_t* src_seq, const int32_t* dst_seq,
-                              int64_t units, const int32_t* keep, const int32_t* n_keep, int keep_stride, int32_t* st,
-                              cudaStream_t stream) {
-  switch (g.nb * g.sb) {   // a power of two: 1 to 32 bytes
-    case 1: return launch_compact<CV, uint8_t>(g, c, src_seq, dst_seq, units, keep, n_keep, keep_stride, st, stream);
-    case 2: return launch_compact<CV, uint16_t>(g, c, src_seq, dst_seq, units, keep, n_keep, keep_stride, st, stream);
-    case 4: return launch_compact<CV, uint32_t>(g, c, src_seq, dst_seq, units, keep, n_keep, keep_stride, st, stream);
-    case 8: return launch_compact<CV, uint2>(g, c, src_seq, dst_seq, units, keep, n_keep, keep_stride, st, stream);
-    default: return launch_compact<CV, uint4>(g, c, src_seq, dst_seq, units, keep, n_keep, keep_stride, st, stream);
+// A token's scales take d/64 (one-byte scales, blocks of 64) to d/8 bytes
+// (fp32, blocks of 32), a power of two.
+template <int D, typename CV, int CN>
+cudaError_t compact_by_header(const CacheGeom& g, const CompactArgs& a) {
+  switch (g.nb * g.sb) {
+    case 1: if constexpr (D <= 64) return launch_compact<CV, CN, uint8_t, 1>(g, a); break;
+    case 2: if constexpr (D <= 128) return launch_compact<CV, CN, uint16_t, 1>(g, a); break;
+    case 4: return launch_compact<CV, CN, uint32_t, 1>(g, a);
+    case 8: return launch_compact<CV, CN, uint2, 1>(g, a);
+    case 16: if constexpr (D >= 128) return launch_compact<CV, CN, uint4, 1>(g, a); break;
+    case 32: if constexpr (D >= 256) return launch_compact<CV, CN, uint4, 2>(g, a); break;
   }
+  return cudaErrorInvalidValue;
+}
+
+// A code string takes b d / 8 bytes: a multiple of 16 but for 3-bit codes at d = 64.
+template <int D>
+cudaError_t compact_by_codes(const CacheGeom& g, const CompactArgs& a) {
+  if (g.bits == 2) return compact_by_header<D, uint4, D / 64>(g, a);
+  if (g.bits == 4) return compact_by_header<D, uint4, D / 32>(g, a);
+  if constexpr (D == 64) return compact_by_header<D, uint2, 3>(g, a);
+  else return compact_by_header<D, uint4, 3 * D / 128>(g, a);
 }
 
 }  // namespace
@@ -417,21 +477,25 @@ kvq3_status kvq3_remap(const kvq3_cache_desc* desc, const kvq3_cache* cache, con
   if (g.num_pages >= ((int64_t)1 << 31)) return KVQ3_ERR_UNSUPPORTED;
   const RemapWs ws = remap_layout(g, workspace);
   if (!workspace || ws_bytes < ws.bytes || reinterpret_cast<uintptr_t>(workspace) % 256) return KVQ3_ERR_WORKSPACE;
+  const bool small = g.batch <= kSmallRows && (int64_t)g.batch * g.max_pages <= kSmallEntries && g.num_pages <= kSmallPages;
+  const unsigned ctas = small ? 1 : kMapCluster;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = kMapCluster;
+  attr[1].val.clusterDim.x = ctas;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kMapCluster);
+  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kMapThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, remap_kernel, g, cache->page_table, cache->seq_lens, src, new_lens, table_out, lens_out,
-                         ws, dev_status) != cudaSuccess)
-    return KVQ3_ERR_CUDA;
+  cfg.numAttrs = small ? 1 : 2;
+  auto run = [&](auto kernel) {
+    return cudaLaunchKernelEx(&cfg, kernel, g, cache->page_table, cache->seq_lens, src, new_lens, table_out, lens_out, ws,
+                              dev_status);
+  };
+  if ((small ? run(remap_kernel<true>) : run(remap_kernel<false>)) != cudaSuccess) return KVQ3_ERR_CUDA;
   const int64_t items = (int64_t)g.batch * 2 * g.hkv, cap = (int64_t)sm_count() * 8;
   cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min(items, cap)));
   cfg.blockDim = dim3(256);
@@ -452,12 +516,14 @@ kvq3_status kvq3_compact(const kvq3_cache_desc* desc, const kvq3_cache* cache, c
   if (!src_seq || !dst_seq || !keep || !n_keep) return KVQ3_ERR_INVALID_ARG;
   const int64_t units = (int64_t)n_seq * g.hkv, tiles = ((int64_t)keep_stride + kKeepTile - 1) / kKeepTile;
   if (units >= ((int64_t)1 << 31) / tiles) return KVQ3_ERR_UNSUPPORTED;   // one CTA per tile
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // a code string is a multiple of 16 bytes except at d = 64 with 3-bit codes (24)
-  const cudaError_t e = g.cb % 16 == 0
-      ? compact_by_header<uint4>(g, cache, src_seq, dst_seq, units, keep, n_keep, keep_stride, dev_status, st)
-      : compact_by_header<uint2>(g, cache, src_seq, dst_seq, units, keep, n_keep, keep_stride, dev_status, st);
-  return cuda_status(e);
+  const CompactArgs a{cache, src_seq, dst_seq, keep, n_keep, units, keep_stride, dev_status,
+                      static_cast<cudaStream_t>(stream)};
+  switch (g.d) {
+    case 64: return cuda_status(compact_by_codes<64>(g, a));
+    case 128: return cuda_status(compact_by_codes<128>(g, a));
+    case 256: return cuda_status(compact_by_codes<256>(g, a));
+  }
+  return KVQ3_ERR_UNSUPPORTED;
 }
 
 }  // extern "C"

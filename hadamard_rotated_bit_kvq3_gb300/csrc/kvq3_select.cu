@@ -12,9 +12,10 @@
 // accuracy.  Bound by HBM: 4d bytes per (page, kv head) for 4 d G flops.
 //
 // Selection.  One CTA per (sequence, kv head): the scores as order-preserving
-// 32-bit keys, a radix select of the budget-th largest between the forced
-// first and last pages, and one ordered compaction that breaks ties towards
-// the lower page.  A few microseconds of latency, no sort.
+// 32-bit keys (in registers up to 8,192 pages), a radix select of the
+// budget-th largest between the forced first and last pages, and one ordered
+// compaction by ballots that breaks ties towards the lower page.  Bound by
+// latency, a few block barriers of a row of a few thousand keys; no sort.
 #include <math.h>
 
 #include "kvq3_internal.h"
@@ -24,13 +25,15 @@ using namespace kvq3;
 namespace {
 
 constexpr int kScoreWarps = 8;
+constexpr int kScoreRounds = 4;
 
-// D: head dimension; NT: n-tiles of 4 heads x (hi, lo) columns.
+// D: head dimension; NT: n-tiles of 4 heads x (hi, lo) columns.  A CTA takes
+// `span` consecutive tiles of 128 pages of one unit, a warp 16 of each.
 template <int D, int NT>
-__global__ void __launch_bounds__(32 * kScoreWarps)
+__global__ void __launch_bounds__(32 * kScoreWarps, 2)
     page_scores_kernel(const __grid_constant__ RotParams rp, const __grid_constant__ CacheGeom g,
                        const int32_t* __restrict__ page_table, const int32_t* __restrict__ seq_lens,
-                       const __half* __restrict__ bounds, const __half* __restrict__ q, int G, int tiles,
+                       const __half* __restrict__ bounds, const __half* __restrict__ q, int G, int groups, int span,
                        float* __restrict__ scores, int32_t* status, float inv_sqrt_d) {
   constexpr int K = 2 * D;
   constexpr int ROW = K + 32;                // halves per B column in shared memory: 64 bytes of padding, no conflicts
@@ -38,48 +41,50 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
   constexpr int L = D / E;
   constexpr int GPW = 32 / L;
   constexpr int CH = D / 32;                 // 16-byte loads per lane and row of one bound
+  constexpr int TP = 16 * kScoreWarps;       // pages of a tile
   __shared__ __align__(16) __half qb[NT * 8 * ROW];
   __shared__ float qinv[NT * 4];             // 2^-e of each head, 0 past the last
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   const int j = lane & 3, r = lane >> 2;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t unit = blockIdx.x / tiles;
-  const int tile = (int)(blockIdx.x - unit * tiles);
+  const int64_t unit = blockIdx.x / groups;
+  const int64_t first = (int64_t)(blockIdx.x - unit * groups) * span * TP;
   const int b = (int)(unit / g.hkv), kvh = (int)(unit - (int64_t)b * g.hkv);
   const int64_t len = seq_lens[b];
   const bool len_ok = len >= 0 && len <= (int64_t)g.max_pages * g.page_size;
   if (!len_ok && threadIdx.x == 0) set_status(status, KVQ3_DEV_BAD_LEN);
   const int64_t n = len_ok ? (len + g.page_size - 1) / g.page_size : 0;
   float* row_out = scores + unit * g.max_pages;
-  const int64_t p0 = (int64_t)tile * (16 * kScoreWarps) + wid * 16;   // this warp's pages
-  if ((int64_t)tile * (16 * kScoreWarps) >= n) {                      // nothing there for the whole CTA
-    const int64_t i = (int64_t)tile * (16 * kScoreWarps) + threadIdx.x;
-    if (threadIdx.x < 16 * kScoreWarps && i < g.max_pages) row_out[i] = -INFINITY;
-    return;
-  }
-  // rows r and r + 8 of the tile: pages p0 + r, p0 + r + 8
-  int64_t page[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int64_t lp = p0 + r + 8 * e;
-    page[e] = lp < n ? page_of(g, page_table, b, lp) : -1;
-    if (lp < n && page[e] < 0 && j == 0) set_status(status, KVQ3_DEV_BAD_PAGE);
-  }
-  const uint4* src[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-    src[e] = reinterpret_cast<const uint4*>(bounds + (page[e] < 0 ? 0 : ((page[e] * g.hkv + kvh) * 2) * D)) + j;
+  const int64_t end = min(first + (int64_t)span * TP, (int64_t)g.max_pages);   // the CTA's pages [first, end)
+  for (int64_t i = max(first, n) + threadIdx.x; i < end; i += 32 * kScoreWarps) row_out[i] = -INFINITY;
+  if (first >= n) return;
+
+  // rows r and r + 8 of this warp's 16 pages of a tile
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  // the first bound's rows are on their way while the query is rotated
+  auto page_at = [&](int64_t lp) {
+    const int64_t p = lp < n ? page_of(g, page_table, b, lp) : -1;
+    if (lp < n && p < 0 && j == 0) set_status(status, KVQ3_DEV_BAD_PAGE);
+    return p;
+  };
+  auto row_of = [&](int64_t page) {
+    return reinterpret_cast<const uint4*>(bounds + (page < 0 ? 0 : ((page * g.hkv + kvh) * 2) * D)) + j;
+  };
+  int64_t p0 = first + wid * 16 + r;
+  int64_t page[2] = {page_at(p0), page_at(p0 + 8)};
+  // the first bound's rows are on their way while the query is rotated; from
+  // then on each row's registers are refilled as they are used: the second
+  // bound's rows, then the next tile's first
   uint4 a[2][CH];
 #pragma unroll
-  for (int e = 0; e < 2; ++e)
+  for (int e = 0; e < 2; ++e) {
+    const uint4* src = row_of(page[e]);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) a[e][c] = page[e] >= 0 ? __ldg(src[e] + 4 * c) : zero;
+    for (int c = 0; c < CH; ++c) a[e][c] = page[e] >= 0 ? __ldg(src + 4 * c) : zero;
+  }
 
   // q1 of the G heads, its negative part against lo and its positive part
-  // against hi, scaled by a power of two into (2^7, 2^8] and split hi + lo
+  // against hi, scaled by a power of two into [2^7, 2^8) and split hi + lo
   {
     const int rq = lane % L, gq = lane / L;
     const uint32_t sgn = lane_signs<E>(rp, rq);
@@ -123,62 +128,93 @@ __global__ void __launch_bounds__(32 * kScoreWarps)
   }
   __syncthreads();
 
-  float acc[NT][4];
+  for (int it = 0; it < span && first + (int64_t)it * TP < n; ++it) {
+    const int64_t p1 = p0 + TP;
+    int64_t next[2] = {-1, -1};
+    if (it + 1 < span) {
+      next[0] = page_at(p1);
+      next[1] = page_at(p1 + 8);
+    }
+    // chains of 8 products at most: a longer one in the tensor core's
+    // accumulator rounds every step to its running sum (1.5e-6 of the score at
+    // 32 steps), so each chain is added to the total in fp32
+    float sum[NT][4];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+    for (int t = 0; t < NT; ++t) sum[t][0] = sum[t][1] = sum[t][2] = sum[t][3] = 0.0f;
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 2; ++s) {
+      const uint4* src[2] = {s == 0 ? row_of(page[0]) + D / 8 : row_of(next[0]),
+                             s == 0 ? row_of(page[1]) + D / 8 : row_of(next[1])};
+      const bool there[2] = {(s == 0 ? page[0] : next[0]) >= 0, (s == 0 ? page[1] : next[1]) >= 0};
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const uint4 x = a[0][c], y = a[1][c];
-      if (s == 0) {   // the second bound's row in the first one's registers
-        a[0][c] = page[0] >= 0 ? __ldg(src[0] + D / 8 + 4 * c) : zero;
-        a[1][c] = page[1] >= 0 ? __ldg(src[1] + D / 8 + 4 * c) : zero;
-      }
-      const uint32_t f0[4] = {x.x, y.x, x.y, y.y}, f1[4] = {x.z, y.z, x.w, y.w};
+      for (int c0 = 0; c0 < CH; c0 += 4) {
+        float acc[NT][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const uint4 w = *reinterpret_cast<const uint4*>(qb + (8 * t + r) * ROW + s * D + 32 * c + 8 * j);
-        mma_16816(acc[t], f0, w.x, w.y);
-        mma_16816(acc[t], f1, w.z, w.w);
+        for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = acc[t][2] = acc[t][3] = 0.0f;
+#pragma unroll
+        for (int c = c0; c < c0 + 4 && c < CH; ++c) {
+          const uint4 x = a[0][c], y = a[1][c];
+          a[0][c] = there[0] ? __ldg(src[0] + 4 * c) : zero;
+          a[1][c] = there[1] ? __ldg(src[1] + 4 * c) : zero;
+          const uint32_t f0[4] = {x.x, y.x, x.y, y.y}, f1[4] = {x.z, y.z, x.w, y.w};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            const uint4 w = *reinterpret_cast<const uint4*>(qb + (8 * t + r) * ROW + s * D + 32 * c + 8 * j);
+            mma_16816(acc[t], f0, w.x, w.y);
+            mma_16816(acc[t], f1, w.z, w.w);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[t][i] += acc[t][i];
       }
     }
-  }
-  float best0 = -INFINITY, best1 = -INFINITY;
+    float best0 = -INFINITY, best1 = -INFINITY;
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const float f = qinv[4 * t + j];
-    if (4 * t + j < G) {
-      best0 = fmaxf(best0, (acc[t][0] + acc[t][1]) * f);
-      best1 = fmaxf(best1, (acc[t][2] + acc[t][3]) * f);
+    for (int t = 0; t < NT; ++t) {
+      const float f = qinv[4 * t + j];
+      if (4 * t + j < G) {
+        best0 = fmaxf(best0, (sum[t][0] + sum[t][1]) * f);
+        best1 = fmaxf(best1, (sum[t][2] + sum[t][3]) * f);
+      }
     }
-  }
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    best0 = fmaxf(best0, __shfl_xor_sync(kFull, best0, o));
-    best1 = fmaxf(best1, __shfl_xor_sync(kFull, best1, o));
-  }
-  if (j < 2) {
-    const int64_t i = p0 + r + 8 * j;
-    if (i < g.max_pages) row_out[i] = (j ? page[1] : page[0]) >= 0 ? (j ? best1 : best0) : -INFINITY;
+    for (int o = 1; o < 4; o <<= 1) {
+      best0 = fmaxf(best0, __shfl_xor_sync(kFull, best0, o));
+      best1 = fmaxf(best1, __shfl_xor_sync(kFull, best1, o));
+    }
+    if (j < 2) {
+      const int64_t i = p0 + 8 * j;
+      if (i < n) row_out[i] = (j ? page[1] : page[0]) >= 0 ? (j ? best1 : best0) : -INFINITY;
+    }
+    p0 = p1;
+    page[0] = next[0];
+    page[1] = next[1];
   }
 }
 
 template <int D, int NT>
 cudaError_t launch_scores(const RotParams& rp, const CacheGeom& g, const kvq3_cache* c, const __half* bounds,
                           const __half* q, int G, float* scores, int32_t* st, cudaStream_t stream) {
-  const int tiles = (int)(((int64_t)g.max_pages + 16 * kScoreWarps - 1) / (16 * kScoreWarps));
+  // tiles a CTA takes: up to 8 while that leaves kScoreRounds CTAs for each
+  // resident one (the query is rotated once a CTA)
+  const int64_t tiles = ((int64_t)g.max_pages + 16 * kScoreWarps - 1) / (16 * kScoreWarps);
+  const int64_t units = (int64_t)g.batch * g.hkv;
+  int span = 1;
+  while (span < 8 && units * ((tiles + 2 * span - 1) / (2 * span)) >= (int64_t)kScoreRounds * 2 * sm_count()) span *= 2;
+  const int groups = (int)((tiles + span - 1) / span);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)g.batch * g.hkv * tiles));
+  cfg.gridDim = dim3((unsigned)(units * groups));
   cfg.blockDim = dim3(32 * kScoreWarps);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, page_scores_kernel<D, NT>, rp, g, c->page_table, c->seq_lens, bounds, q, G, tiles,
-                            scores, st, inv_sqrt(D));
+  return cudaLaunchKernelEx(&cfg, page_scores_kernel<D, NT>, rp, g, c->page_table, c->seq_lens, bounds, q, G, groups,
+                            span, scores, st, inv_sqrt(D));
 }
 
 template <int D>
@@ -191,8 +227,8 @@ cudaError_t scores_by_heads(const RotParams& rp, const CacheGeom& g, const kvq3_
 
 // ------------------------------------------------------------ selection
 constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;          // 11 bits a pass: 11 + 11 + 10
-constexpr int kSelCache = 8192;      // keys held in shared memory (longer rows are read again)
 
 // Order-preserving key: larger score, larger key; NaN lowest, -0 as +0.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -201,43 +237,35 @@ __device__ __forceinline__ uint32_t score_key(float x) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Exclusive block sum of v over the threads; *total receives the sum.
-__device__ __forceinline__ uint32_t block_excl(uint32_t v, uint32_t* wsum, uint32_t* total) {
-  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  uint32_t incl = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t t = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += t;
-  }
-  __syncthreads();
-  if (lane == 31) wsum[wid] = incl;
-  __syncthreads();
-  uint32_t base = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kSelThreads / 32; ++w) {
-    const uint32_t t = wsum[w];
-    base += w < wid ? t : 0u;
-    all += t;
-  }
-  *total = all;
-  return base + incl - v;
-}
-
+// Keys of a row's competing pages, page i = k kSelThreads + thread in round k:
+// in registers for rows of up to KPT rounds (the kernel's template), read
+// again from memory each time for longer ones (KPT = 0).
+template <int KPT>
 __global__ void __launch_bounds__(kSelThreads)
     page_select_kernel(const __grid_constant__ CacheGeom g, const int32_t* __restrict__ seq_lens,
                        const float* __restrict__ scores, int budget, int sinks, int recent, int32_t* __restrict__ pages,
                        int32_t* __restrict__ counts, int32_t* status) {
-  __shared__ uint32_t keys[kSelCache];
   __shared__ uint32_t hist[kBins];
-  __shared__ uint32_t wsum[kSelThreads / 32];
-  __shared__ uint32_t found[2];
+  __shared__ uint32_t wsum[kSelWarps];
+  __shared__ uint2 found;
+  __shared__ uint2 wcount[(KPT > 0 ? KPT : 1) * kSelWarps];   // larger and equal keys of each warp and round
+  const int t = threadIdx.x, lane = t & 31, wid = t >> 5;
+  for (int i = t; i < kBins; i += kSelThreads) hist[i] = 0;
   griddep_wait();
   griddep_launch_dependents();
-  const int t = threadIdx.x;
   const int64_t unit = blockIdx.x;
   const int b = (int)(unit / g.hkv);
+  const float* row = scores + unit * g.max_pages + sinks;
   const int64_t len = seq_lens[b];
+  // the scores do not wait for the length: every page of the row can be read
+  float raw[KPT > 0 ? KPT : 1];
+  if constexpr (KPT > 0) {
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+      const int i = k * kSelThreads + t;
+      raw[k] = i < g.max_pages - sinks ? row[i] : 0.0f;
+    }
+  }
   const bool len_ok = len >= 0 && len <= (int64_t)g.max_pages * g.page_size;
   if (!len_ok && t == 0) set_status(status, KVQ3_DEV_BAD_LEN);
   const int n = len_ok ? (int)((len + g.page_size - 1) / g.page_size) : 0;
@@ -249,71 +277,143 @@ __global__ void __launch_bounds__(kSelThreads)
   }
   // pages [sinks, n - recent) compete for `want` places; 0 <= want < m
   const int m = n - sinks - recent, want = budget - sinks - recent;
-  const float* row = scores + unit * g.max_pages + sinks;
   for (int i = t; i < sinks; i += kSelThreads) out[i] = i;
   for (int i = t; i < recent; i += kSelThreads) out[budget - recent + i] = n - recent + i;
   if (want == 0) return;
-  const bool cached = m <= kSelCache;
-  if (cached)
-    for (int i = t; i < m; i += kSelThreads) keys[i] = score_key(row[i]);
-  auto key_at = [&](int i) { return cached ? keys[i] : score_key(row[i]); };
+  const int rounds = (m + kSelThreads - 1) / kSelThreads;   // <= KPT where KPT > 0
+  uint32_t key[KPT > 0 ? KPT : 1];
+  if constexpr (KPT > 0) {
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) key[k] = score_key(raw[k]);
+  }
+  // f(key, page, round) for this thread's pages
+  auto each = [&](auto f) {
+    if constexpr (KPT > 0) {
+#pragma unroll
+      for (int k = 0; k < KPT; ++k) {
+        const int i = k * kSelThreads + t;
+        if (i < m) f(key[k], i, k);
+      }
+    } else {
+      for (int i = t; i < m; i += kSelThreads) f(score_key(row[i]), i, 0);
+    }
+  };
 
-  // radix select of the want-th largest key: bits [31..21], [20..10], [9..0]
-  uint32_t prefix = 0, left = (uint32_t)want;   // places left within the prefix
-  uint32_t equal = 0;                           // keys equal to the one found, at the end
+  // radix select of the want-th largest key, bits [31..21], [20..10], [9..0]:
+  // ends as soon as the places left take all of a bin
+  uint32_t low = 0, left = (uint32_t)want, equal = 0;   // keys >= low are in, of those == low the first `equal`
+  uint32_t prefix = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const int bins = pass == 2 ? 1024 : kBins;
-    for (int i = t; i < bins; i += kSelThreads) hist[i] = 0;
+    const uint32_t mask = pass == 2 ? 1023u : kBins - 1u;
+    if (pass > 0)
+      for (int i = t; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
-    for (int i = t; i < m; i += kSelThreads) {
-      const uint32_t k = key_at(i);
-      if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == prefix) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+    each([&](uint32_t k, int, int) {
+      if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1u);
+    });
+    __syncthreads();
+    // from the top, four bins a thread: the bin that holds the left-th
+    constexpr int PER = kBins / kSelThreads;
+    const uint4 h4 = *reinterpret_cast<const uint4*>(&hist[kBins - PER * (t + 1)]);   // bins ascending
+    const uint32_t h[PER] = {h4.w, h4.z, h4.y, h4.x};
+    const uint32_t mine = h[0] + h[1] + h[2] + h[3];
+    uint32_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
     }
+    if (lane == 31) wsum[wid] = incl;
     __syncthreads();
-    // from the top: the bin that holds the left-th
-    const int per = bins / kSelThreads, top = bins - 1 - t * per;
-    uint32_t mine = 0;
-    for (int i = 0; i < per; ++i) mine += hist[top - i];
-    uint32_t total;
-    uint32_t above = block_excl(mine, wsum, &total);
+    uint32_t above = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) above += w < wid ? wsum[w] : 0u;
     if (above < left && left <= above + mine) {
-      for (int i = 0; i < per; ++i) {
-        const uint32_t h = hist[top - i];
-        if (left <= above + h) {
-          found[0] = (uint32_t)(top - i);
-          found[1] = left - above;
-          break;
-        }
-        above += h;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (above < left && left <= above + h[i])
+          found = make_uint2((uint32_t)(kBins - 1 - PER * t - i) | (left - above == h[i] ? 1u << 31 : 0u), left - above);
+        above += h[i];
       }
     }
     __syncthreads();
-    prefix = pass == 0 ? found[0] : (prefix << (pass == 1 ? 11 : 10)) | found[0];
-    left = found[1];
-    __syncthreads();
+    const uint2 f = found;
+    const uint32_t bin = f.x & 0x7fffffffu;
+    prefix = pass == 0 ? bin : (prefix << (pass == 1 ? 11 : 10)) | bin;
+    left = f.y;
+    low = prefix << shift;
+    equal = left;
+    if (f.x >> 31) {   // the whole bin is in: every key at or above its lowest
+      equal = 0xffffffffu;
+      break;
+    }
   }
-  equal = left;   // of the keys equal to `prefix`, the first `equal` by page
 
-  // each thread a run of consecutive pages: larger keys and, in order, the
-  // first of the equal ones
-  const int per = (m + kSelThreads - 1) / kSelThreads;
-  const int i0 = min(m, t * per), i1 = min(m, i0 + per);
-  uint32_t gt = 0, eq = 0;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key_at(i);
-    gt += k > prefix;
-    eq += k == prefix;
-  }
-  uint32_t total;
-  const uint32_t gt0 = block_excl(gt, wsum, &total);
-  uint32_t eq0 = block_excl(eq, wsum, &total);
-  uint32_t at = (uint32_t)sinks + gt0 + min(eq0, equal);
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key_at(i);
-    const bool take = k > prefix || (k == prefix && eq0++ < equal);
-    if (take) out[at++] = sinks + i;
+  // in page order: keys above `low` and the first `equal` of those at it (all
+  // of them, when a whole bin was taken: then every key >= low counts)
+  const bool whole = equal == 0xffffffffu;
+  auto larger = [&](uint32_t k) { return whole ? k >= low : k > low; };
+  auto same = [&](uint32_t k) { return !whole && k == low; };
+  const uint32_t below = (1u << lane) - 1u;
+  if constexpr (KPT > 0) {
+    uint32_t gt[KPT], eq[KPT];
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+      const bool in = k * kSelThreads + t < m;
+      gt[k] = __ballot_sync(kFull, in && larger(key[k]));
+      eq[k] = __ballot_sync(kFull, in && same(key[k]));
+      if (lane == 0) wcount[k * kSelWarps + wid] = make_uint2(__popc(gt[k]), __popc(eq[k]));
+    }
+    __syncthreads();
+    if (wid == 0) {   // exclusive sums over (round, warp)
+      uint2 base = make_uint2(0, 0);
+      for (int i0 = 0; i0 < KPT * kSelWarps; i0 += 32) {
+        const uint2 c = i0 + lane < KPT * kSelWarps ? wcount[i0 + lane] : make_uint2(0, 0);
+        uint2 s = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t x = __shfl_up_sync(kFull, s.x, o), y = __shfl_up_sync(kFull, s.y, o);
+          if (lane >= o) {
+            s.x += x;
+            s.y += y;
+          }
+        }
+        if (i0 + lane < KPT * kSelWarps) wcount[i0 + lane] = make_uint2(base.x + s.x - c.x, base.y + s.y - c.y);
+        base.x += __shfl_sync(kFull, s.x, 31);
+        base.y += __shfl_sync(kFull, s.y, 31);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < KPT; ++k) {
+      const uint2 c = wcount[k * kSelWarps + wid];
+      const uint32_t g0 = c.x + __popc(gt[k] & below), e0 = c.y + __popc(eq[k] & below);
+      const bool is_gt = (gt[k] >> lane) & 1u, is_eq = (eq[k] >> lane) & 1u;
+      if (is_gt || (is_eq && e0 < equal)) out[sinks + g0 + min(e0, equal)] = sinks + k * kSelThreads + t;
+    }
+  } else {
+    uint32_t g_all = 0, e_all = 0;   // before this round
+    for (int k = 0; k < rounds; ++k) {
+      const int i = k * kSelThreads + t;
+      const uint32_t kk = i < m ? score_key(row[i]) : 0u;
+      const uint32_t gt = __ballot_sync(kFull, i < m && larger(kk)), eq = __ballot_sync(kFull, i < m && same(kk));
+      __syncthreads();
+      if (lane == 0) wcount[wid] = make_uint2(__popc(gt), __popc(eq));
+      __syncthreads();
+      uint32_t g0 = g_all + __popc(gt & below), e0 = e_all + __popc(eq & below);
+#pragma unroll
+      for (int w = 0; w < kSelWarps; ++w) {
+        const uint2 c = wcount[w];
+        g0 += w < wid ? c.x : 0u;
+        e0 += w < wid ? c.y : 0u;
+        g_all += c.x;
+        e_all += c.y;
+      }
+      const bool is_gt = (gt >> lane) & 1u, is_eq = (eq >> lane) & 1u;
+      if (is_gt || (is_eq && e0 < equal)) out[sinks + g0 + min(e0, equal)] = sinks + i;
+    }
   }
 }
 
@@ -368,8 +468,15 @@ kvq3_status kvq3_page_select(const kvq3_cache_desc* desc, const kvq3_cache* cach
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, page_select_kernel, g, cache->seq_lens, scores, budget, sinks, recent,
-                                        pages, counts, dev_status));
+  // the rounds that the longest row can take
+  auto run = [&](auto kernel) {
+    return cuda_status(cudaLaunchKernelEx(&cfg, kernel, g, cache->seq_lens, scores, budget, sinks, recent, pages, counts,
+                                          dev_status));
+  };
+  if (g.max_pages <= kSelThreads) return run(page_select_kernel<1>);
+  if (g.max_pages <= 4 * kSelThreads) return run(page_select_kernel<4>);
+  if (g.max_pages <= 16 * kSelThreads) return run(page_select_kernel<16>);
+  return run(page_select_kernel<0>);
 }
 
 }  // extern "C"
