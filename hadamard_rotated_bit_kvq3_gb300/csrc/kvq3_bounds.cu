@@ -25,10 +25,7 @@ using namespace kvq3;
 namespace {
 
 constexpr int kThreads = 128;
-#ifndef KLT
-#define KLT 32
-#endif
-constexpr int kLaneTokens = KLT;
+constexpr int kLaneTokens = 32;
 constexpr int kSeg = 1024;   // sequences whose page counts are held in shared memory at a time
 
 // Page count of every sequence of a segment as an inclusive running sum in
@@ -344,15 +341,16 @@ __global__ void __launch_bounds__(kThreads)
             ss[u] = load_scale<SCALE>(scales + (uint32_t)(t * tb));
           }
         };
+        const int step = U * sub;
         load(s, c, sc);
-        for (int t0 = s; t0 < n; t0 += U * sub) {
-          if (t0 + U * sub < n) load(t0 + U * sub, cn, scn);
+        for (int t0 = s; t0 < n; t0 += 2 * step) {
+          if (t0 + step < n) load(t0 + step, cn, scn);
 #pragma unroll
           for (int u = 0; u < U; ++u) acc.add(c[u], sc[u]);
+          if (t0 + step < n) {
+            if (t0 + 2 * step < n) load(t0 + 2 * step, c, sc);
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            c[u] = cn[u];
-            sc[u] = scn[u];
+            for (int u = 0; u < U; ++u) acc.add(cn[u], scn[u]);
           }
         }
       }
