@@ -371,25 +371,29 @@ kvq3_status pages_view(const CacheGeom& g, int32_t hq, int32_t row, CacheGeom* v
 
 // CTAs per unit of the cluster form, 0 for the flattened one.  The costs are in
 // units of one chunk's time on a busy SM (1.1 to 1.3 us): a wave of CTAs pays
-// about 6.5 to start and to merge, an SM needs about 2.4 chunks in flight to
-// be busy, and the flattened form pays about 26 for its list, partials and
-// second kernel but divides the chunks evenly over all CTAs.  Measured (us),
+// about 6.5 to start and to merge; an SM is busy with about 2.4 chunks in
+// flight where it holds 4 CTAs, and with as many as it holds where registers
+// allow fewer; the flattened form pays about 26 for its list, partials and
+// second kernel but divides the chunks evenly over all CTAs.  Measured (us):
 // 128 units of 16 chunks at 4 CTAs an SM: 1, 2, 3, 4, 8 CTAs a unit 43.4,
-// 27.5, 32.9, 25.6, 30.2, flattened 39.6; 64 units of 64 chunks at 3 an SM: 4,
-// 5, 6, 8 CTAs 67.8, 58.9, 51.0, 69.0, flattened 65.3.
+// 27.5, 32.9, 25.6, 30.2, flattened 39.6; 64 units of 64 chunks at 3 an SM
+// (G = 8): 4, 5, 6, 8 CTAs 67.8, 58.9, 51.0, 69.0, flattened 65.3; 256 units of
+// 16 chunks at 3 an SM (d = 256): 1, 2, 3, 4 CTAs 66.1, 65.8, 60.0, 64.3,
+// flattened 83.8.
 int pages_parts(const DecodePlan& plan, int64_t units, int32_t row) {
   const int sms = std::max(1, sm_count());
   const int per_sm = std::max(1, plan.ctas / sms);
+  const double busy = per_sm >= 4 ? 2.4 : 0.97 * per_sm;
   const int64_t nc = ((int64_t)row + plan.pages_per_chunk - 1) / plan.pages_per_chunk;
-  double best = 26.0 + std::max(2.4, (double)per_sm) * (double)((units * nc + plan.ctas - 1) / plan.ctas);
+  double best = 26.0 + per_sm * (double)((units * nc + plan.ctas - 1) / plan.ctas);
   int parts = 0;
   for (int n = 1; n <= 8 && n <= nc; ++n) {
     if (plan.clusters[n] < 1) continue;
     const int64_t waves = (units + plan.clusters[n] - 1) / plan.clusters[n];
     const int64_t last = units - (waves - 1) * plan.clusters[n];   // clusters of the last wave
     const double k = (double)((nc + n - 1) / n);
-    const double cost = waves * 6.5 + (waves - 1) * k * std::max(2.4, (double)per_sm) +
-                        k * std::max(2.4, (double)((last * n + sms - 1) / sms));
+    const double cost = waves * 6.5 + (waves - 1) * k * per_sm +
+                        k * std::max(busy, (double)((last * n + sms - 1) / sms));
     if (cost < best) {
       best = cost;
       parts = n;

@@ -12,7 +12,7 @@
 // accuracy.  Bound by HBM: 4d bytes per (page, kv head) for 4 d G flops.
 //
 // Selection.  One CTA per (sequence, kv head): the scores as order-preserving
-// 32-bit keys (in registers up to 8,192 pages), a radix select of the
+// 32-bit keys (in registers up to 8,192 pages), a histogram search for the
 // budget-th largest between the forced first and last pages, and one ordered
 // compaction by ballots that breaks ties towards the lower page.  Bound by
 // latency, a few block barriers of a row of a few thousand keys; no sort.
@@ -228,7 +228,8 @@ cudaError_t scores_by_heads(const RotParams& rp, const CacheGeom& g, const kvq3_
 // ------------------------------------------------------------ selection
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;          // 11 bits a pass: 11 + 11 + 10
+constexpr int kBins = 2048;
+constexpr int kBinBits = 11;
 
 // Order-preserving key: larger score, larger key; NaN lowest, -0 as +0.
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -247,7 +248,10 @@ __global__ void __launch_bounds__(kSelThreads)
                        int32_t* __restrict__ counts, int32_t* status) {
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t wsum[kSelWarps];
-  __shared__ uint2 found;
+  __shared__ uint2 range_s[kSelWarps];   // smallest and largest key of each warp
+  __shared__ uint4 found;                // bin, places left in it, its keys
+  __shared__ uint32_t n_cand;
+  __shared__ unsigned long long cand[32];
   __shared__ uint2 wcount[(KPT > 0 ? KPT : 1) * kSelWarps];   // larger and equal keys of each warp and round
   const int t = threadIdx.x, lane = t & 31, wid = t >> 5;
   for (int i = t; i < kBins; i += kSelThreads) hist[i] = 0;
@@ -299,19 +303,40 @@ __global__ void __launch_bounds__(kSelThreads)
     }
   };
 
-  // radix select of the want-th largest key, bits [31..21], [20..10], [9..0]:
-  // ends as soon as the places left take all of a bin
-  uint32_t low = 0, left = (uint32_t)want, equal = 0;   // keys >= low are in, of those == low the first `equal`
-  uint32_t prefix = 0;
+  // The want-th largest key, by a histogram over the range that holds it: the
+  // keys of a row differ in few of their top bits, so the first bins divide
+  // [smallest, largest] instead of all 32-bit keys (and are not a handful of
+  // contended counters).  Each pass narrows the range to one bin of the last;
+  // it ends when the bin is taken whole, when 32 keys or fewer are left (one
+  // warp ranks them by key, then page), or when they are all equal.
+  uint32_t kmin = 0xffffffffu, kmax = 0;
+  each([&](uint32_t k, int, int) {
+    kmin = min(kmin, k);
+    kmax = max(kmax, k);
+  });
+  kmin = __reduce_min_sync(kFull, kmin);
+  kmax = __reduce_max_sync(kFull, kmax);
+  if (lane == 0) range_s[wid] = make_uint2(kmin, kmax);
+  if (t == 0) n_cand = 0;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSelWarps; ++w) {
+    const uint2 v = range_s[w];
+    kmin = min(kmin, v.x);
+    kmax = max(kmax, v.y);
+  }
+  uint32_t base = kmin, span = kmax - kmin;       // the keys [base, base + span] hold the one looked for
+  uint32_t left = (uint32_t)want;                 // its rank among them
+  uint32_t low = 0, at = 0xffffffffu, equal = 0;  // in: keys above low; at low, pages up to `at` (or the first `equal`)
+  bool whole = false;                             // in: keys from low on
 #pragma unroll 1
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    const uint32_t mask = pass == 2 ? 1023u : kBins - 1u;
+  for (int pass = 0;; ++pass) {
+    const int shift = max(0, 32 - __clz((int)span) - kBinBits);   // span >> shift < kBins
     if (pass > 0)
       for (int i = t; i < kBins; i += kSelThreads) hist[i] = 0;
     __syncthreads();
     each([&](uint32_t k, int, int) {
-      if (pass == 0 || (k >> (pass == 1 ? 21 : 10)) == prefix) atomicAdd(&hist[(k >> shift) & mask], 1u);
+      if (k - base <= span) atomicAdd(&hist[(k - base) >> shift], 1u);
     });
     __syncthreads();
     // from the top, four bins a thread: the bin that holds the left-th
@@ -334,35 +359,56 @@ __global__ void __launch_bounds__(kSelThreads)
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         if (above < left && left <= above + h[i])
-          found = make_uint2((uint32_t)(kBins - 1 - PER * t - i) | (left - above == h[i] ? 1u << 31 : 0u), left - above);
+          found = make_uint4((uint32_t)(kBins - 1 - PER * t - i), left - above, h[i], 0);
         above += h[i];
       }
     }
     __syncthreads();
-    const uint2 f = found;
-    const uint32_t bin = f.x & 0x7fffffffu;
-    prefix = pass == 0 ? bin : (prefix << (pass == 1 ? 11 : 10)) | bin;
+    const uint4 f = found;
+    base += f.x << shift;
+    span = (shift ? (1u << shift) : 1u) - 1u;   // may reach past the last pass's range, where no key is
     left = f.y;
-    low = prefix << shift;
-    equal = left;
-    if (f.x >> 31) {   // the whole bin is in: every key at or above its lowest
-      equal = 0xffffffffu;
+    low = base;
+    if (f.y == f.z) {
+      whole = true;
+      break;
+    }
+    if (span == 0) {
+      equal = left;
+      break;
+    }
+    if (f.z <= 32) {
+      each([&](uint32_t k, int i, int) {
+        if (k - base <= span) cand[atomicAdd(&n_cand, 1u)] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)i);
+      });
+      __syncthreads();
+      // every warp ranks the candidates: larger key first, lower page first
+      const unsigned long long c = lane < f.z ? cand[lane] : 0ull;
+      uint32_t rank = 0;
+#pragma unroll
+      for (int o = 0; o < 32; ++o) rank += __shfl_sync(kFull, c, o) > c;
+      const int src = __ffs(__ballot_sync(kFull, lane < f.z && rank == left - 1u)) - 1;
+      const unsigned long long last = __shfl_sync(kFull, c, src);
+      low = (uint32_t)(last >> 32);
+      at = 0xffffffffu - (uint32_t)last;
       break;
     }
   }
 
-  // in page order: keys above `low` and the first `equal` of those at it (all
-  // of them, when a whole bin was taken: then every key >= low counts)
-  const bool whole = equal == 0xffffffffu;
-  auto larger = [&](uint32_t k) { return whole ? k >= low : k > low; };
-  auto same = [&](uint32_t k) { return !whole && k == low; };
+  // in page order: keys above `low`, and at it the pages up to `at` or the
+  // first `equal` of them (a bin taken whole: every key from `low` on)
+  const bool by_page = !whole && equal == 0;
+  auto larger = [&](uint32_t k, int i) {
+    return whole ? k >= low : k > low || (by_page && k == low && (uint32_t)i <= at);
+  };
+  auto same = [&](uint32_t k) { return equal != 0 && k == low; };
   const uint32_t below = (1u << lane) - 1u;
   if constexpr (KPT > 0) {
     uint32_t gt[KPT], eq[KPT];
 #pragma unroll
     for (int k = 0; k < KPT; ++k) {
       const bool in = k * kSelThreads + t < m;
-      gt[k] = __ballot_sync(kFull, in && larger(key[k]));
+      gt[k] = __ballot_sync(kFull, in && larger(key[k], k * kSelThreads + t));
       eq[k] = __ballot_sync(kFull, in && same(key[k]));
       if (lane == 0) wcount[k * kSelWarps + wid] = make_uint2(__popc(gt[k]), __popc(eq[k]));
     }
@@ -398,7 +444,7 @@ __global__ void __launch_bounds__(kSelThreads)
     for (int k = 0; k < rounds; ++k) {
       const int i = k * kSelThreads + t;
       const uint32_t kk = i < m ? score_key(row[i]) : 0u;
-      const uint32_t gt = __ballot_sync(kFull, i < m && larger(kk)), eq = __ballot_sync(kFull, i < m && same(kk));
+      const uint32_t gt = __ballot_sync(kFull, i < m && larger(kk, i)), eq = __ballot_sync(kFull, i < m && same(kk));
       __syncthreads();
       if (lane == 0) wcount[wid] = make_uint2(__popc(gt), __popc(eq));
       __syncthreads();
@@ -473,9 +519,11 @@ kvq3_status kvq3_page_select(const kvq3_cache_desc* desc, const kvq3_cache* cach
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, g, cache->seq_lens, scores, budget, sinks, recent, pages, counts,
                                           dev_status));
   };
-  if (g.max_pages <= kSelThreads) return run(page_select_kernel<1>);
-  if (g.max_pages <= 4 * kSelThreads) return run(page_select_kernel<4>);
-  if (g.max_pages <= 16 * kSelThreads) return run(page_select_kernel<16>);
+  const int64_t most = (int64_t)g.max_pages - sinks - recent;
+  if (most <= kSelThreads) return run(page_select_kernel<1>);
+  if (most <= 3 * kSelThreads) return run(page_select_kernel<3>);
+  if (most <= 8 * kSelThreads) return run(page_select_kernel<8>);
+  if (most <= 16 * kSelThreads) return run(page_select_kernel<16>);
   return run(page_select_kernel<0>);
 }
 
