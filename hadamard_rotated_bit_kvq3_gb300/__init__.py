@@ -20,8 +20,7 @@ __all__ = [
     "kvq3_cache_sizes", "kvq3_rotate", "kvq3_write", "kvq3_write_chunk", "kvq3_decode_workspace_size",
     "kvq3_decode_attn", "kvq3_decode_attn_noalloc", "kvq3_prefill_workspace_size", "kvq3_prefill_attn",
     "kvq3_dequant_debug", "kvq3_calib_sse", "kvq3_calibrate_workspace_size", "kvq3_calibrate_so4", "Rotation",
-    "kvq3_key_bounds", "kvq3_page_scores", "kvq3_page_select", "kvq3_decode_pages_workspace_size",
-    "kvq3_decode_attn_pages", "kvq3_remap_workspace_size", "kvq3_remap", "kvq3_compact",
+    "kvq3_key_bounds", "kvq3_page_scores", "kvq3_page_select", "kvq3_decode_attn_pages", "kvq3_remap_workspace_size", "kvq3_remap", "kvq3_compact",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -92,8 +91,7 @@ _SIGS = {
     "kvq3_key_bounds": (ctypes.c_int, [_D, _C, _p, _p, _p, _p]),
     "kvq3_page_scores": (ctypes.c_int, [_p, _D, _C, _p, _p, _i32, _p, _p, _p]),
     "kvq3_page_select": (ctypes.c_int, [_D, _C, _p, _i32, _i32, _i32, _p, _p, _p, _p]),
-    "kvq3_decode_pages_workspace_size": (ctypes.c_int, [_D, _i32, _i32, ctypes.POINTER(_sz)]),
-    "kvq3_decode_attn_pages": (ctypes.c_int, [_p, _D, _C, _p, _i32, _f32, _p, _p, _i32, _p, _p, _sz, _p, _p]),
+    "kvq3_decode_attn_pages": (ctypes.c_int, [_p, _D, _C, _p, _i32, _f32, _p, _p, _i32, _p, _p, _p]),
     "kvq3_remap_workspace_size": (ctypes.c_int, [_D, ctypes.POINTER(_sz)]),
     "kvq3_remap": (ctypes.c_int, [_D, _C, _p, _p, _p, _p, _p, _sz, _p, _p]),
     "kvq3_compact": (ctypes.c_int, [_D, _C, _p, _p, _i32, _p, _p, _i32, _p, _p]),
@@ -412,25 +410,17 @@ def kvq3_page_select(desc: CacheDesc, cache: Cache, scores, budget: int, sinks: 
         _word(dev_status), _raw_stream(stream)), w)
 
 
-def kvq3_decode_pages_workspace_size(desc: CacheDesc, num_q_heads: int, max_selected: int) -> int:
-    n = _sz()
-    _check(lib.kvq3_decode_pages_workspace_size(desc, num_q_heads, max_selected, ctypes.byref(n)),
-           "kvq3_decode_pages_workspace_size")
-    return n.value
-
-
-def kvq3_decode_attn_pages(h, desc: CacheDesc, cache: Cache, q, pages, counts, out, workspace, sm_scale: float = 0.0,
+def kvq3_decode_attn_pages(h, desc: CacheDesc, cache: Cache, q, pages, counts, out, sm_scale: float = 0.0,
                            dev_status=None, stream=None) -> None:
     """q, out: fp16 [B][Hq][d]; pages: int32 [B][Hkv][n], strictly ascending;
-    counts: int32 [B][Hkv]; workspace: uint8 CUDA tensor
-    (kvq3_decode_pages_workspace_size(desc, Hq, n) bytes)."""
+    counts: int32 [B][Hkv]."""
     t, w = _torch(), "kvq3_decode_attn_pages"
     b, hkv, hq, n = desc.batch, desc.num_kv_heads, q.shape[1], pages.shape[2]
     rows = (b, hq, desc.head_dim)
     _check(lib.kvq3_decode_attn_pages(
         h, desc, cache, _at(q, "q", t.float16, rows, w), hq, sm_scale, _at(pages, "pages", t.int32, (b, hkv, n), w),
         _at(counts, "counts", t.int32, (b, hkv), w), n, _at(out, "out", t.float16, rows, w),
-        *_workspace(workspace, w), _word(dev_status), _raw_stream(stream)), w)
+        _word(dev_status), _raw_stream(stream)), w)
 
 
 def _workspace(ws, where: str):

@@ -302,99 +302,36 @@ kvq3_status kvq3_test_prefill_attn_polls(kvq3_rotation rot, const kvq3_cache_des
 }  // extern "C"
 
 // ------------------------------------------------------------------ selected pages
-// Attention over selected pages has two forms.  The cluster form (SEL of the
-// decode kernel) is one launch: 1 to 8 CTAs per (sequence, kv head), merged
-// through the cluster's shared memory.  Where there are so few units, with
-// lists so long, that 8 CTAs a unit leave most of the GPU idle, the flattened
-// form runs the dense decode kernel on another view of the same pool: a record pair (K and V of one page and kv head) is a page of its
-// own, number page * Hkv + kv head, and every (sequence, kv head) a sequence
-// of one kv head whose page table is its list.  The list is ascending, so only
-// its last page can be part filled, and the view's length says how far.
+// Attention over selected pages: the SEL form of the decode kernel, a cluster
+// of 1 to 16 CTAs per (sequence, kv head).
 namespace {
 
-constexpr int kListThreads = 256;
-
-// The view's page table [units][row] and lengths [units].
-__global__ void __launch_bounds__(kListThreads)
-    page_list_kernel(const __grid_constant__ CacheGeom g, const int32_t* __restrict__ page_table,
-                     const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ pages,
-                     const int32_t* __restrict__ counts, int32_t row, int32_t* __restrict__ vtable,
-                     int32_t* __restrict__ vlens, int32_t* status) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int64_t units = (int64_t)g.batch * g.hkv, total = units * row;
-  const int64_t cap = (int64_t)g.max_pages * g.page_size;
-  for (int64_t k = (int64_t)blockIdx.x * kListThreads + threadIdx.x; k < total; k += (int64_t)gridDim.x * kListThreads) {
-    const int64_t u = k / row;
-    const int i = (int)(k - u * row);
-    const int b = (int)(u / g.hkv), kvh = (int)(u - (int64_t)b * g.hkv);
-    const int64_t len = seq_lens[b];
-    int c = counts[u];
-    if (len < 0 || len > cap || c < 0 || c > row) {
-      if (i == 0) set_status(status, KVQ3_DEV_BAD_LEN);
-      c = 0;
-    }
-    int64_t page = -1;
-    bool part = false;
-    if (i < c) {
-      const int64_t lp = pages[k];
-      // a page of the sequence, above the entry before it; a part-filled page can only be the last one
-      if (lp >= 0 && lp * g.page_size < len && (i == 0 || lp > pages[k - 1])) {
-        part = (lp + 1) * g.page_size > len;
-        if (!part || i == c - 1) page = page_of(g, page_table, b, lp);
-      }
-      if (page < 0) set_status(status, KVQ3_DEV_BAD_PAGE);
-    }
-    vtable[k] = page < 0 ? -1 : (int32_t)(page * g.hkv + kvh);
-    // tokens of the view: every listed page whole, but the last one up to the length
-    if (c == 0 ? i == 0 : i == c - 1)
-      vlens[u] = c == 0 ? 0 : (int32_t)((int64_t)c * g.page_size - (part && page >= 0 ? g.page_size - len % g.page_size : 0));
-  }
-}
-
-// The view's geometry; KVQ3_ERR_UNSUPPORTED where an index would pass 31 bits.
-kvq3_status pages_view(const CacheGeom& g, int32_t hq, int32_t row, CacheGeom* v) {
-  kvq3_status s = check_heads(g, hq);
-  if (s != KVQ3_OK) return s;
-  if (row < 1) return KVQ3_ERR_INVALID_ARG;
-  const int64_t lim = (int64_t)1 << 31;
-  if (g.num_pages >= lim / g.hkv || (int64_t)g.batch * hq >= lim || (int64_t)row * g.page_size >= lim)
-    return KVQ3_ERR_UNSUPPORTED;
-  *v = g;
-  v->hkv = 1;
-  v->batch = g.batch * g.hkv;
-  v->max_pages = row;
-  v->num_pages = g.num_pages * g.hkv;
-  v->page_bytes = 2 * g.record_bytes;
-  return KVQ3_OK;
-}
-
-// CTAs per unit of the cluster form, 0 for the flattened one.  The costs are in
-// units of one chunk's time on a busy SM (1.1 to 1.3 us): a wave of CTAs pays
-// about 6.5 to start and to merge; an SM is busy with about 2.4 chunks in
-// flight where it holds 4 CTAs, and with as many as it holds where registers
-// allow fewer; the flattened form pays about 26 for its list, partials and
-// second kernel but divides the chunks evenly over all CTAs.  Measured (us):
-// 128 units of 16 chunks at 4 CTAs an SM: 1, 2, 3, 4, 8 CTAs a unit 43.4,
-// 27.5, 32.9, 25.6, 30.2, flattened 39.6; 64 units of 64 chunks at 3 an SM
-// (G = 8): 4, 5, 6, 8 CTAs 67.8, 58.9, 51.0, 69.0, flattened 65.3; 256 units of
-// 16 chunks at 3 an SM (d = 256): 1, 2, 3, 4 CTAs 66.1, 65.8, 60.0, 64.3,
-// flattened 83.8.
+// CTAs per unit.  The costs are in units of one chunk's time on a busy SM (1.1
+// to 1.3 us): a wave of CTAs pays about 6.5 to start and to merge, and an SM is
+// busy with about 2.4 chunks in flight where it holds 4 CTAs, with as many as
+// it holds where registers allow fewer; clusters spread over the SMs to within
+// about 5 %.  Measured (us): 128 units of 16 chunks at 4 CTAs an SM: 1, 2, 3,
+// 4, 8 CTAs a unit 43.4, 27.5, 32.9, 25.6, 30.2; 64 units of 64 chunks at 3 an
+// SM (G = 8): 4, 5, 6, 8 CTAs 67.8, 58.9, 51.0, 69.0; 256 units of 16 chunks at
+// 3 an SM (d = 256): 1, 2, 3, 4 CTAs 66.1, 65.8, 60.0, 64.3; 1,024 units of 16
+// chunks: 1, 2, 4 CTAs 131, 136, 150; 8 units of 16 chunks: 2, 4, 8 CTAs 21.7,
+// 13.5, 9.2.  (The dense kernel's even split over all CTAs with a second
+// merging kernel took 39.6, 65.3, 83.8, 169 and 18.7.)
 int pages_parts(const DecodePlan& plan, int64_t units, int32_t row) {
   const int sms = std::max(1, sm_count());
   const int per_sm = std::max(1, plan.ctas / sms);
   const double busy = per_sm >= 4 ? 2.4 : 0.97 * per_sm;
   const int64_t nc = ((int64_t)row + plan.pages_per_chunk - 1) / plan.pages_per_chunk;
-  double best = 26.0 + per_sm * (double)((units * nc + plan.ctas - 1) / plan.ctas);
-  int parts = 0;
-  for (int n = 1; n <= 8 && n <= nc; ++n) {
-    if (plan.clusters[n] < 1) continue;
+  double best = 0.0;
+  int parts = 1;
+  for (int n : {1, 2, 3, 4, 6, 8, 12, 16}) {   // (others leave SMs more unevenly filled)
+    if (n > nc || plan.clusters[n] < 1) continue;
     const int64_t waves = (units + plan.clusters[n] - 1) / plan.clusters[n];
     const int64_t last = units - (waves - 1) * plan.clusters[n];   // clusters of the last wave
     const double k = (double)((nc + n - 1) / n);
     const double cost = waves * 6.5 + (waves - 1) * k * per_sm +
-                        k * std::max(busy, (double)((last * n + sms - 1) / sms));
-    if (cost < best) {
+                        k * std::max(busy, ceil((double)last * n * 1.05 / sms));
+    if (n == 1 || cost < best) {
       best = cost;
       parts = n;
     }
@@ -402,107 +339,55 @@ int pages_parts(const DecodePlan& plan, int64_t units, int32_t row) {
   return parts;
 }
 
-// Bytes of the view's table and lengths ahead of the decode workspace.
-size_t view_bytes(const CacheGeom& v) { return ((size_t)v.batch * ((size_t)v.max_pages + 1) * 4 + 255) / 256 * 256; }
+kvq3_status decode_pages_impl(kvq3_rotation rot, const kvq3_cache_desc* desc, const kvq3_cache* cache, const void* q,
+                              int32_t num_q_heads, float sm_scale, const int32_t* pages, const int32_t* counts,
+                              int32_t max_selected, void* out, int32_t* dev_status, void* stream, uint32_t wait_limit) {
+  CacheGeom g;
+  kvq3_status s = make_geom(desc, &g);
+  if (s != KVQ3_OK) return s;
+  if (!rot || rot->d != g.d || !q || !out || !pages || !counts || max_selected < 1) return KVQ3_ERR_INVALID_ARG;
+  if ((s = check_cache(g, cache, true)) != KVQ3_OK) return s;
+  if ((s = check_heads(g, num_q_heads)) != KVQ3_OK) return s;
+  if (!(sm_scale <= 0.0f || isfinite(sm_scale))) return KVQ3_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) % 16 != 0) return KVQ3_ERR_INVALID_ARG;
+  const int64_t lim = (int64_t)1 << 31;   // 32-bit unit, query row and token counts
+  if ((int64_t)g.batch * num_q_heads >= lim || (int64_t)max_selected * g.page_size >= lim) return KVQ3_ERR_UNSUPPORTED;
+  const int G = num_q_heads / g.hkv;
+  DecodePlan plan;
+  if ((s = pages_plan_for(g, G, &plan)) != KVQ3_OK) return s;
+  DecodeParams prm;
+  memset(&prm, 0, sizeof(prm));
+  prm.g = g;
+  prm.pool = static_cast<const uint8_t*>(cache->pool);
+  prm.page_table = cache->page_table;
+  prm.seq_lens = cache->seq_lens;
+  prm.q = static_cast<const __half*>(q);
+  prm.status = dev_status;
+  prm.G = G;
+  prm.Hq = num_q_heads;
+  const double sc = sm_scale > 0.0f ? (double)sm_scale : 1.0 / sqrt((double)g.d);
+  prm.qk_scale = (float)(sc * 1.4426950408889634);  // log2(e): softmax in base 2
+  prm.inv_sqrt_d = inv_sqrt(g.d);
+  prm.wait_limit = wait_limit;
+  prm.sel_pages = pages;
+  prm.sel_counts = counts;
+  prm.sel_row = max_selected;
+  prm.sel_parts = pages_parts(plan, (int64_t)g.batch * g.hkv, max_selected);
+  prm.sel_out = static_cast<__half*>(out);
+  if ((int64_t)g.batch * g.hkv >= lim / prm.sel_parts) return KVQ3_ERR_UNSUPPORTED;   // the grid
+  return pages_run_for(g, plan, prm, rot->params, static_cast<cudaStream_t>(stream));
+}
 
 }  // namespace
 
 extern "C" {
 
-kvq3_status kvq3_decode_pages_workspace_size(const kvq3_cache_desc* desc, int32_t num_q_heads, int32_t max_selected,
-                                             size_t* bytes) {
-  CacheGeom g, v;
-  kvq3_status s = make_geom(desc, &g);
-  if (s != KVQ3_OK) return s;
-  if (!bytes) return KVQ3_ERR_INVALID_ARG;
-  if ((s = pages_view(g, num_q_heads, max_selected, &v)) != KVQ3_OK) return s;
-  const int G = num_q_heads / g.hkv;
-  DecodePlan plan;
-  if ((s = pages_plan_for(g, G, &plan)) != KVQ3_OK) return s;
-  *bytes = 256;   // the cluster form needs none
-  if (pages_parts(plan, v.batch, max_selected) > 0) return KVQ3_OK;
-  if ((s = plan_for(v, G, &plan)) != KVQ3_OK) return s;
-  *bytes = view_bytes(v) + plan.ws_bytes;
-  return KVQ3_OK;
-}
-
-static kvq3_status decode_pages_impl(kvq3_rotation rot, const kvq3_cache_desc* desc, const kvq3_cache* cache,
-                                     const void* q, int32_t num_q_heads, float sm_scale, const int32_t* pages,
-                                     const int32_t* counts, int32_t max_selected, void* out, void* workspace,
-                                     size_t ws_bytes, int32_t* dev_status, void* stream, uint32_t wait_limit) {
-  CacheGeom g, v;
-  kvq3_status s = make_geom(desc, &g);
-  if (s != KVQ3_OK) return s;
-  if (!rot || rot->d != g.d || !q || !out || !pages || !counts) return KVQ3_ERR_INVALID_ARG;
-  if ((s = check_cache(g, cache, true)) != KVQ3_OK) return s;
-  if ((s = pages_view(g, num_q_heads, max_selected, &v)) != KVQ3_OK) return s;
-  if (!(sm_scale <= 0.0f || isfinite(sm_scale))) return KVQ3_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(out)) % 16 != 0) return KVQ3_ERR_INVALID_ARG;
-  const int G = num_q_heads / g.hkv;
-  DecodePlan plan;
-  if ((s = pages_plan_for(g, G, &plan)) != KVQ3_OK) return s;
-  const int parts = pages_parts(plan, v.batch, max_selected);
-  if (parts == 0 && (s = plan_for(v, G, &plan)) != KVQ3_OK) return s;
-  const size_t head = view_bytes(v);
-  if (!workspace || ws_bytes < (parts ? 256 : head + plan.ws_bytes) || reinterpret_cast<uintptr_t>(workspace) % 256)
-    return KVQ3_ERR_WORKSPACE;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  DecodeParams prm;
-  memset(&prm, 0, sizeof(prm));
-  prm.pool = static_cast<const uint8_t*>(cache->pool);
-  prm.q = static_cast<const __half*>(q);
-  prm.status = dev_status;
-  prm.G = G;
-  const double sc = sm_scale > 0.0f ? (double)sm_scale : 1.0 / sqrt((double)g.d);
-  prm.qk_scale = (float)(sc * 1.4426950408889634);  // log2(e): softmax in base 2
-  prm.inv_sqrt_d = inv_sqrt(g.d);
-  prm.wait_limit = wait_limit;
-  if (parts > 0) {
-    prm.g = g;
-    prm.page_table = cache->page_table;
-    prm.seq_lens = cache->seq_lens;
-    prm.Hq = num_q_heads;
-    prm.sel_pages = pages;
-    prm.sel_counts = counts;
-    prm.sel_row = max_selected;
-    prm.sel_parts = parts;
-    prm.sel_out = static_cast<__half*>(out);
-    return pages_run_for(g, plan, prm, rot->params, st);
-  }
-
-  int32_t* vtable = static_cast<int32_t*>(workspace);
-  int32_t* vlens = vtable + (size_t)v.batch * v.max_pages;
-  char* ws = static_cast<char*>(workspace) + head;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  const int64_t blocks = ((int64_t)v.batch * v.max_pages + kListThreads - 1) / kListThreads;
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(blocks, (int64_t)sm_count() * 8));
-  cfg.blockDim = dim3(kListThreads);
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, page_list_kernel, g, cache->page_table, cache->seq_lens, pages, counts, max_selected,
-                         vtable, vlens, dev_status) != cudaSuccess)
-    return KVQ3_ERR_CUDA;
-  prm.g = v;
-  prm.page_table = vtable;
-  prm.seq_lens = vlens;
-  prm.ws = reinterpret_cast<float*>(ws);
-  prm.unit_cta = reinterpret_cast<int32_t*>(ws + ((size_t)plan.ctas + (size_t)v.batch) * G * (g.d + 2) * sizeof(float));
-  prm.Hq = G;
-  prm.slot_floats = (uint32_t)(G * (g.d + 2));
-  prm.out_half = 1;
-  return run_for(v, plan, prm, rot->params, static_cast<float*>(out), st);
-}
-
 kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc* desc, const kvq3_cache* cache,
                                    const void* q, int32_t num_q_heads, float sm_scale, const int32_t* pages,
-                                   const int32_t* counts, int32_t max_selected, void* out, void* workspace,
-                                   size_t ws_bytes, int32_t* dev_status, void* stream) {
-  return decode_pages_impl(rot, desc, cache, q, num_q_heads, sm_scale, pages, counts, max_selected, out, workspace,
-                           ws_bytes, dev_status, stream, kWaitPolls);
+                                   const int32_t* counts, int32_t max_selected, void* out, int32_t* dev_status,
+                                   void* stream) {
+  return decode_pages_impl(rot, desc, cache, q, num_q_heads, sm_scale, pages, counts, max_selected, out, dev_status,
+                           stream, kWaitPolls);
 }
 
 // Test hook, not part of the public header: kvq3_decode_attn_pages with the
@@ -510,10 +395,10 @@ kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc* des
 // kvq3_test_decode_attn_polls.
 kvq3_status kvq3_test_decode_pages_polls(kvq3_rotation rot, const kvq3_cache_desc* desc, const kvq3_cache* cache,
                                          const void* q, int32_t num_q_heads, float sm_scale, const int32_t* pages,
-                                         const int32_t* counts, int32_t max_selected, void* out, void* workspace,
-                                         size_t ws_bytes, int32_t* dev_status, void* stream, uint32_t polls) {
-  return decode_pages_impl(rot, desc, cache, q, num_q_heads, sm_scale, pages, counts, max_selected, out, workspace,
-                           ws_bytes, dev_status, stream, polls);
+                                         const int32_t* counts, int32_t max_selected, void* out, int32_t* dev_status,
+                                         void* stream, uint32_t polls) {
+  return decode_pages_impl(rot, desc, cache, q, num_q_heads, sm_scale, pages, counts, max_selected, out, dev_status,
+                           stream, polls);
 }
 
 }  // extern "C"

@@ -55,6 +55,7 @@ constexpr int kChunk = 192;      // minimum tokens per chunk (smaller pages are 
 constexpr int kMaxPagesPerChunk = kChunk / 16;
 constexpr int kWarps = 4;        // consumer warps per CTA
 constexpr int kMaxStages = 8;
+constexpr int kMaxParts = 16;   // CTAs of a unit's cluster (SEL)
 
 struct DecodeParams {
   CacheGeom g;
@@ -99,7 +100,6 @@ struct DecodeParams {
   int32_t sel_row;
   int32_t sel_parts;
   __half* sel_out;
-  int32_t out_half;       // the combine kernel writes fp16 (the flattened form of the same)
 };
 
 // ------------------------------------------------------------------ helpers
@@ -1728,6 +1728,7 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
     const int rank = (int)(blockIdx.x - (unsigned)unit * (unsigned)parts);
     const uint32_t sgn = lane_signs<EQ>(rp, rq);
     const int ns = parts * kWarps;   // states of the unit: at most 64, two a lane
+    static_assert(kMaxParts * kWarps <= 64, "two states a lane");
     const uint32_t ml_a = smem_u32(ml_s), part_a = smem_u32(part_s);
     for (int h = rank + parts * wid; h < p.G; h += parts * kWarps) {
       float mv[2], lv[2];
@@ -1865,11 +1866,7 @@ __global__ void __launch_bounds__(256) decode_combine_kernel(const __grid_consta
     rotate_inverse<E, L>(o, rr, sgn, qt, qtr, p.inv_sqrt_d, so4, pair);
     if (grp == 0) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const int64_t at = (int64_t)it * D + rr * E + e;
-        if (p.out_half) reinterpret_cast<__half*>(out)[at] = __float2half_rn(o[e]);
-        else out[at] = o[e];
-      }
+      for (int e = 0; e < E; ++e) out[(int64_t)it * D + rr * E + e] = o[e];
     }
   }
 }
@@ -1882,7 +1879,7 @@ struct DecodePlan {
   int chunk_tokens, pages_per_chunk;
   uint32_t stage_bytes, smem;
   size_t ws_bytes;
-  int clusters[9];   // SEL: resident clusters of 1..8 CTAs
+  int clusters[kMaxParts + 1];   // SEL: resident clusters of 1..16 CTAs
 };
 
 template <int D, int BLOCK, int GPAD, int SCALE, int NBIT, bool PSPLIT, bool PF = false, bool SEL = false>
@@ -2024,7 +2021,9 @@ kvq3_status pages_plan_t(const CacheGeom& g, int G, DecodePlan* plan) {
     const kvq3_status s = decode_plan_t<D, BLOCK, GPAD, SCALE, NBIT, PSPLIT, false, true>(g, G, &kept.plan);
     if (s != KVQ3_OK) return s;
     auto* k = &decode_split_kernel<D, BLOCK, GPAD, SCALE, NBIT, PSPLIT, false, true>;
-    for (int n = 1; n <= 8; ++n) {
+    // clusters of more than 8 CTAs need the kernel's consent
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return KVQ3_ERR_CUDA;
+    for (int n = 1; n <= kMaxParts; ++n) {
       cudaLaunchAttribute attr[1];
       attr[0].id = cudaLaunchAttributeClusterDimension;
       attr[0].val.clusterDim.x = (unsigned)n;

@@ -471,8 +471,13 @@ kvq3_status kvq3_remap(const kvq3_cache_desc* desc, const kvq3_cache* cache, con
   kvq3_status s = make_geom(desc, &g);
   if (s != KVQ3_OK) return s;
   if ((s = check_cache(g, cache, true)) != KVQ3_OK) return s;
-  if (!cache->page_table || !src || !new_lens || !table_out || !lens_out || table_out == cache->page_table ||
-      lens_out == cache->seq_lens)
+  if (!cache->page_table || !src || !new_lens || !table_out || !lens_out) return KVQ3_ERR_INVALID_ARG;
+  // the old table and lengths are read while the new ones are written
+  auto apart = [](const int32_t* a, const int32_t* b, int64_t n) {
+    return reinterpret_cast<uintptr_t>(a) + n * 4 <= reinterpret_cast<uintptr_t>(b) ||
+           reinterpret_cast<uintptr_t>(b) + n * 4 <= reinterpret_cast<uintptr_t>(a);
+  };
+  if (!apart(table_out, cache->page_table, (int64_t)g.batch * g.max_pages) || !apart(lens_out, cache->seq_lens, g.batch))
     return KVQ3_ERR_INVALID_ARG;
   if (g.num_pages >= ((int64_t)1 << 31)) return KVQ3_ERR_UNSUPPORTED;
   const RemapWs ws = remap_layout(g, workspace);

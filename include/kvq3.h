@@ -499,11 +499,6 @@ kvq3_status kvq3_page_select(const kvq3_cache_desc *desc, const kvq3_cache *cach
                              const float *scores, int32_t budget, int32_t sinks, int32_t recent,
                              int32_t *pages, int32_t *counts, int32_t *dev_status, void *stream);
 
-/* Device workspace bytes of kvq3_decode_attn_pages with lists of up to
- * max_selected pages. */
-kvq3_status kvq3_decode_pages_workspace_size(const kvq3_cache_desc *desc, int32_t num_q_heads,
-                                             int32_t max_selected, size_t *bytes);
-
 /* kvq3_decode_attn over selected pages: each query head of kv head h of
  * sequence b attends to the positions below seq_lens[b] of the pages
  * pages[b][h][0 .. counts[b][h]).  pages: device int32
@@ -514,15 +509,15 @@ kvq3_status kvq3_decode_pages_workspace_size(const kvq3_cache_desc *desc, int32_
  * (KVQ3_DEV_BAD_LEN), and so does an empty list.
  * q: device fp16 [batch][Hq][d]; out: device fp16 [batch][Hq][d], what the
  * projection after it reads (one rounding of the fp32 result, 2^-11 relative,
- * below the error bar of the attention); both 16-byte aligned.  workspace: device, 256-byte
- * aligned, ws_bytes >= kvq3_decode_pages_workspace_size; calls sharing it must
- * not overlap.  The rest as for kvq3_decode_attn; KVQ3_ERR_UNSUPPORTED when
- * num_pages * Hkv, batch * Hq or max_selected * P reaches 2^31. */
+ * below the error bar of the attention); both 16-byte aligned.  No workspace:
+ * one launch, whose partial results meet on chip, added in a fixed order (the
+ * same call gives the same bits).  The rest as for kvq3_decode_attn;
+ * KVQ3_ERR_UNSUPPORTED when batch * Hq or max_selected * P reaches 2^31. */
 kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc *desc,
                                    const kvq3_cache *cache, const void *q, int32_t num_q_heads,
                                    float sm_scale, const int32_t *pages, const int32_t *counts,
-                                   int32_t max_selected, void *out, void *workspace,
-                                   size_t ws_bytes, int32_t *dev_status, void *stream);
+                                   int32_t max_selected, void *out, int32_t *dev_status,
+                                   void *stream);
 
 /* ---- Pages of a paged cache: forking, growing, truncating, freeing and
  * compacting sequences (a page table is required).
@@ -541,9 +536,9 @@ kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc *des
  *     A page is free when no row of the new table holds it: there is no other
  *     allocation state, and a page held outside the table (a kept prefix)
  *     is one that some row of the batch holds.
- * table_out: device int32 [batch][max_pages_per_seq], not the cache's table
- * (KVQ3_ERR_INVALID_ARG), -1 past new_lens[b]; lens_out: device int32
- * [batch] = held, not the cache's lengths.  The caller then uses the two in
+ * table_out: device int32 [batch][max_pages_per_seq], apart from the cache's
+ * table (KVQ3_ERR_INVALID_ARG), -1 past new_lens[b]; lens_out: device int32
+ * [batch] = held, apart from the cache's lengths.  The caller then uses the two in
  * place of the cache's page_table and seq_lens.  Contents of a page beyond
  * the tokens it held are left as they were; key bounds of a copied page are
  * not copied (kvq3_key_bounds makes them).

@@ -266,12 +266,9 @@ def test_page_select_bad_length():
 def _attend(c, q, pages, counts, sm=0.0):
     t = c.torch
     full, out = c.guarded(q.shape, t.float16, 9.0)
-    n_ws = c.K.kvq3_decode_pages_workspace_size(c.desc, q.shape[1], pages.shape[2])
-    ws = t.full((n_ws + CANARY,), CANARY_BYTE, dtype=t.uint8, device="cuda")
-    c.K.kvq3_decode_attn_pages(c.rot.handle, c.desc, c.cache, c.dev(q), c.dev(pages), c.dev(counts), out, ws[:n_ws], sm,
-                               c.status)
+    c.K.kvq3_decode_attn_pages(c.rot.handle, c.desc, c.cache, c.dev(q), c.dev(pages), c.dev(counts), out, sm, c.status)
     t.cuda.synchronize()
-    assert bool((full[-64:] == 9.0).all()) and bool((ws[n_ws:] == CANARY_BYTE).all())
+    assert bool((full[-64:] == 9.0).all())
     c.pool_now()
     return out.cpu().numpy().astype(np.float64)
 
@@ -315,7 +312,7 @@ ATTN = [
     (dict(lens=(333, 20, 64), scale="e4m3zp", paged=False), 4, 4),
     (dict(lens=(5000, 4999, 3), page=16, hkv=8), 4, 200),
     (dict(lens=tuple(5 + 7 * i for i in range(70)), page=16, hkv=4), 4, 4),   # many short units
-    # few units with long lists: the flattened form
+    # few units with long lists: up to 16 CTAs a unit
     (dict(lens=(40000,), page=16, hkv=1), 4, 2600),
     (dict(lens=(60000, 300), page=64, hkv=1, scale="e4m3", flags=7), 8, 800),
     (dict(lens=(33000, 0, 17), page=16, hkv=1, scale="e4m3zp", d=64, block=32), 3, 2000),
@@ -347,7 +344,7 @@ def test_all_pages_is_the_dense_decode():
     _near(got, out.cpu().numpy().astype(np.float64))
 
 
-@pytest.mark.parametrize("row", [5, 40000])   # the cluster form, and (long lists of few units) the flattened one
+@pytest.mark.parametrize("row", [5, 40000])   # short lists, and short ones in long rows (16 CTAs a unit, most idle)
 def test_decode_attn_pages_bad_lists(row):
     c = Pages(lens=(100, 100, 100, 100, 100, 50), hkv=1, page=16, maxp=8)
     q = c.queries(4)
@@ -387,10 +384,9 @@ def test_decode_attn_pages_wait_that_runs_out(kw, G, row):
     pages, counts = _lists(c, row)
     qd, pd, nd = c.dev(q), c.dev(pages), c.dev(counts)
     out = t.empty(q.shape, dtype=t.float16, device="cuda")
-    ws = t.empty(K.kvq3_decode_pages_workspace_size(c.desc, q.shape[1], row), dtype=t.uint8, device="cuda")
     for _ in range(2):
         assert fn(c.rot.handle, c.desc, c.cache, qd.data_ptr(), q.shape[1], 0.0, pd.data_ptr(), nd.data_ptr(), row,
-                  out.data_ptr(), ws.data_ptr(), ws.numel(), c.status.data_ptr(), K._raw_stream(None), 0) == 0
+                  out.data_ptr(), c.status.data_ptr(), K._raw_stream(None), 0) == 0
         t.cuda.synchronize()
         assert c.flags() & K.DEV_BITS["timeout"]
         c.status.zero_()
@@ -549,8 +545,7 @@ def _step_buffers(c, G, budget):
     return dict(
         scores=t.empty(*heads, c.maxp, device="cuda"), pages=t.empty(*heads, budget, dtype=t.int32, device="cuda"),
         counts=t.empty(*heads, dtype=t.int32, device="cuda"),
-        out=t.empty(c.B, c.hkv * G, c.d, dtype=t.float16, device="cuda"),
-        ws=t.empty(c.K.kvq3_decode_pages_workspace_size(c.desc, c.hkv * G, budget), dtype=t.uint8, device="cuda"))
+        out=t.empty(c.B, c.hkv * G, c.d, dtype=t.float16, device="cuda"))
 
 
 def _step(c, cache, b, bounds, first, k, v, seq, pos, q, budget):
@@ -560,7 +555,7 @@ def _step(c, cache, b, bounds, first, k, v, seq, pos, q, budget):
     K.kvq3_key_bounds(c.desc, cache, first, bounds, c.status)
     K.kvq3_page_scores(c.rot.handle, c.desc, cache, bounds, q, b["scores"], c.status)
     K.kvq3_page_select(c.desc, cache, b["scores"], budget, 1, 1, b["pages"], b["counts"], c.status)
-    K.kvq3_decode_attn_pages(c.rot.handle, c.desc, cache, q, b["pages"], b["counts"], b["out"], b["ws"], 0.0, c.status)
+    K.kvq3_decode_attn_pages(c.rot.handle, c.desc, cache, q, b["pages"], b["counts"], b["out"], 0.0, c.status)
 
 
 @pytest.mark.parametrize("how", ["eager", "side stream", "graph"])
@@ -643,8 +638,8 @@ def test_serving_loop(how):
             assert np.array_equal(O.read_rotated(after, L, 0, h, w, 0, 40, last)[1], want)
 
 
-def test_two_streams_with_their_own_workspaces():
-    # the same cache read by two streams at once
+def test_two_streams():
+    # the same cache read by two streams at once (the attention has no workspace to share)
     c = Pages(lens=(700, 333, 64), page=16, hkv=2)
     t, G, row = c.torch, 4, 12
     q1, q2 = c.queries(G, 1), c.queries(G, 2)
@@ -656,7 +651,7 @@ def test_two_streams_with_their_own_workspaces():
     t.cuda.synchronize()
     for _ in range(20):
         for s, q, p, n, b in run:
-            c.K.kvq3_decode_attn_pages(c.rot.handle, c.desc, c.cache, q, p, n, b["out"], b["ws"], 0.0, c.status, stream=s)
+            c.K.kvq3_decode_attn_pages(c.rot.handle, c.desc, c.cache, q, p, n, b["out"], 0.0, c.status, stream=s)
     t.cuda.synchronize()
     assert c.flags() == 0
     for q, p, n, r in ((q1, p1, n1, run[0]), (q2, p2, n2, run[1])):

@@ -71,17 +71,14 @@ def test_decode_attn_pages_refusals(K):
     rot, rot64 = K.Rotation(128, 1), K.Rotation(64, 1)
     def call(desc=None, hq=8, n=4, r=rot.handle, q=A, pages=A, counts=B, out=C, sm=0.0, cache=None):   # noqa: E306
         return K.lib.kvq3_decode_attn_pages(r, ctypes.byref(desc or _desc(K)), ctypes.byref(cache or _cache(K)), q, hq, sm,
-                                            pages, counts, n, out, None, 0, None, None)
+                                            pages, counts, n, out, None, None)
     for kw in (dict(r=None), dict(r=rot64.handle), dict(q=None), dict(pages=None), dict(counts=None), dict(out=None),
                dict(hq=0), dict(hq=9), dict(n=0), dict(n=-3), dict(sm=float("inf")), dict(cache=_cache(K, lens=None)),
                dict(q=ctypes.c_void_p(4104)), dict(out=ctypes.c_void_p(4098))):
         assert call(**kw) == INVALID, kw
     assert call(hq=34) == UNSUPPORTED
     assert call(n=(1 << 31) // 16) == UNSUPPORTED                               # a list of 2^31 tokens
-    assert call(desc=_desc(K, num_pages=(1 << 30))) == UNSUPPORTED              # 2^31 (page, kv head) pairs
     assert call(desc=_desc(K, batch=(1 << 28))) == UNSUPPORTED                  # 2^31 query rows
-    with pytest.raises(K.Kvq3Error):
-        K.kvq3_decode_pages_workspace_size(_desc(K), 8, 0)
 
 
 def test_remap_refusals_and_workspace(K):
@@ -96,7 +93,8 @@ def test_remap_refusals_and_workspace(K):
         return K.lib.kvq3_remap(ctypes.byref(desc), ctypes.byref(cache or _cache(K)), src, new, table_out, lens_out, ws,
                                 n_ws, None, None)
     for kw in (dict(src=None), dict(new=None), dict(table_out=None), dict(lens_out=None), dict(table_out=table),
-               dict(lens_out=lens), dict(cache=_cache(K, table=None)), dict(cache=_cache(K, lens=None))):
+               dict(table_out=ctypes.c_void_p(8192 + 44)), dict(table_out=ctypes.c_void_p(8192 - 4)),
+               dict(lens_out=lens), dict(lens_out=ctypes.c_void_p(12288 + 8)), dict(cache=_cache(K, table=None)), dict(cache=_cache(K, lens=None))):
         assert call(**kw) == INVALID, kw
     for kw in (dict(ws=None), dict(n_ws=need - 1), dict(ws=ctypes.c_void_p(264))):
         assert call(**kw) == WORKSPACE, kw
