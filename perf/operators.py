@@ -244,9 +244,6 @@ def _library(s):
     rot = ws = None
     if "U" in s:
         rot = K.kvq3_rotation_create_from_params(c["d"], s["signs"].cpu().numpy(), s["quats"].cpu().numpy())
-    if c["op"] == "attn":
-        ws = torch.empty(K.kvq3_decode_pages_workspace_size(desc, c["hkv"] * c["group"], c["budget"]), dtype=torch.uint8,
-                         device=DEV)
     if c["op"] == "remap":
         ws = torch.empty(K.kvq3_remap_workspace_size(desc), dtype=torch.uint8, device=DEV)
     return K, desc, cache, rot, ws
@@ -268,7 +265,7 @@ def _run_own(s):
                            s["status"])
         return s["pages"], s["counts"]
     if op == "attn":
-        K.kvq3_decode_attn_pages(rot, desc, cache, s["q"], s["pages"], s["counts"], s["out"], ws, 0.0, s["status"])
+        K.kvq3_decode_attn_pages(rot, desc, cache, s["q"], s["pages"], s["counts"], s["out"], 0.0, s["status"])
         return s["out"]
     if op == "remap":
         K.kvq3_remap(desc, cache, s["src"], s["new_lens"], s["table_out"], s["lens_out"], ws, s["status"])
