@@ -765,13 +765,10 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
                &full[stage], pol);
   };
   if constexpr (SEL) {
-    // each warp fills the stages wid, wid + 4, ..., its first entries read
-    // together with the count and the length
-    int32_t entry = first_entry;
-    for (int64_t i = wid; i < nch && i < S; i += kWarps) {
-      issue(Cursor{sel_b, sel_kvh, c0 + i * p.sel_parts, sel_seq}, (int)i, sel_n, entry);
-      entry = entry_of(sel_unit, c0 + (i + kWarps) * p.sel_parts);
-    }
+    // the first stage now, by warp 0, its entries read together with the count
+    // and the length; the others follow once the query is set up, so that the
+    // first chunk of every CTA on the GPU arrives before the second of any
+    if (wid == 0 && nch > 0) issue(Cursor{sel_b, sel_kvh, c0, sel_seq}, 0, sel_n, first_entry);
   } else {
     Cursor cp = cursor_at(p, c0);  // warp-collective
     if (wid == 0) {
@@ -1528,6 +1525,11 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
     // while the first copies are in flight; the time-out path skips the unit's
     // chunks but not the cluster's merge, so the state is set up in any case
     setup_sel();
+    int32_t entry = first_entry;
+    for (int64_t i = wid; i < nch && i < S; i += kWarps) {   // stages wid, wid + 4, ...
+      if (i > 0) issue(Cursor{sel_b, sel_kvh, c0 + i * p.sel_parts, sel_seq}, (int)i, sel_n, entry);
+      entry = entry_of(sel_unit, c0 + (i + kWarps) * p.sel_parts);
+    }
   }
   const int P = g.page_size;
   int stage = 0;          // i mod S
@@ -1757,22 +1759,33 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
       float o1[EQ];
 #pragma unroll
       for (int e = 0; e < EQ; ++e) o1[e] = 0.0f;
-      for (int i0 = 0; i0 < ns; i0 += kWarps) {   // a CTA's four states
-        float4 v[kWarps][EQ / 4];
+      // the states of four CTAs (two at d = 256) at a time, every load under
+      // way before the first is used
+      constexpr int CG = EQ == 8 ? 2 : 4;
+      for (int i0 = 0; i0 < parts; i0 += CG) {
+        float4 v[CG][kWarps][EQ / 4];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
+        for (int c = 0; c < CG; ++c)
 #pragma unroll
-          for (int e = 0; e < EQ / 4; ++e)
-            v[w][e] = ld_cluster4(part_a + (uint32_t)((w * GPAD + h) * OROW + rq * EQ + 4 * e) * 4u, i0 / kWarps);
+          for (int w = 0; w < kWarps; ++w)
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float c = __shfl_sync(kFull, i0 < 32 ? wv[0] : wv[1], (i0 + w) & 31);
+            for (int e = 0; e < EQ / 4; ++e)
+              if (i0 + c < parts)
+                v[c][w][e] = ld_cluster4(part_a + (uint32_t)((w * GPAD + h) * OROW + rq * EQ + 4 * e) * 4u, i0 + c);
 #pragma unroll
-          for (int e = 0; e < EQ / 4; ++e) {
-            o1[4 * e + 0] = fmaf(c, v[w][e].x, o1[4 * e + 0]);
-            o1[4 * e + 1] = fmaf(c, v[w][e].y, o1[4 * e + 1]);
-            o1[4 * e + 2] = fmaf(c, v[w][e].z, o1[4 * e + 2]);
-            o1[4 * e + 3] = fmaf(c, v[w][e].w, o1[4 * e + 3]);
+        for (int c = 0; c < CG; ++c) {
+          if (i0 + c >= parts) break;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) {
+            const int i = (i0 + c) * kWarps + w;
+            const float f = __shfl_sync(kFull, i < 32 ? wv[0] : wv[1], i & 31);
+#pragma unroll
+            for (int e = 0; e < EQ / 4; ++e) {
+              o1[4 * e + 0] = fmaf(f, v[c][w][e].x, o1[4 * e + 0]);
+              o1[4 * e + 1] = fmaf(f, v[c][w][e].y, o1[4 * e + 1]);
+              o1[4 * e + 2] = fmaf(f, v[c][w][e].z, o1[4 * e + 2]);
+              o1[4 * e + 3] = fmaf(f, v[c][w][e].w, o1[4 * e + 3]);
+            }
           }
         }
       }
