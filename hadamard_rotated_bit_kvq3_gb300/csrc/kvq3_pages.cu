@@ -12,12 +12,14 @@
 //
 // The bookkeeping is a chain of dependent passes over the table and the page
 // bitmap (a few hundred KB at most), bound by the latency of its loads and
-// barriers.  A small table (up to 512 rows and 64K entries) is one CTA's work,
-// with the rows' state and the bitmap in shared memory and block barriers
-// between the passes; a larger one is a thread-block cluster's, its state in
-// the workspace and the hardware cluster barrier between, in one launch.  The copies of part-filled pages are the only bulk
-// traffic; a second kernel, launched as its programmatic dependent, spreads
-// them over the GPU and moves only the slots in use.
+// barriers.  For a small table (up to 512 rows and 64K entries) every CTA of
+// one launch does all of it for itself, with the rows' state and the bitmap in
+// shared memory and block barriers between the passes; the first CTA writes
+// the result, and each then copies its share of the part-filled pages without
+// waiting for another.  A larger table is a thread-block cluster's work, its
+// state in the workspace and the hardware cluster barrier between, and the
+// copies, the only bulk traffic, are a second kernel's, its programmatic
+// dependent.  Only the slots in use are copied.
 //
 // Compaction is a gather of packed vectors (codes and scales as stored); one
 // CTA takes a run of kept tokens of a (sequence, kv head), resolves each
@@ -41,7 +43,8 @@ constexpr int kMapCluster = 8;      // CTAs of the remap cluster (the portable m
 // moves only about 100 GB/s of table.
 constexpr int kSmallRows = 512;
 constexpr int kSmallEntries = 65536;
-constexpr int kSmallPages = 131072;
+constexpr int kSmallPages = 65536;
+constexpr int kCopyPieces = 5;      // pieces of a record's copy: its codes in quarters, its scales
 
 // What the remap keeps in its workspace.
 struct RemapWs {
@@ -100,32 +103,16 @@ __device__ __forceinline__ int64_t cta_excl(int64_t v, int64_t* wsum, int64_t* t
   return base + incl - v;
 }
 
-template <bool SMALL>
 __global__ void __launch_bounds__(kMapThreads)
     remap_kernel(const __grid_constant__ CacheGeom g, const int32_t* table, const int32_t* seq_lens, const int32_t* src,
-                 const int32_t* new_lens, int32_t* table_out, int32_t* lens_out, const __grid_constant__ RemapWs global,
+                 const int32_t* new_lens, int32_t* table_out, int32_t* lens_out, const __grid_constant__ RemapWs ws,
                  int32_t* status) {
   __shared__ int64_t wsum[kMapThreads / 32];
   __shared__ int64_t part[2];   // this CTA's free pages and wanted entries
-  __shared__ uint32_t bits_s[SMALL ? kSmallPages / 32 : 1];
-  __shared__ int64_t first_s[SMALL ? kSmallRows : 1];
-  __shared__ int4 rows_s[SMALL ? kSmallRows : 1];
-  __shared__ int32_t need_s[SMALL ? kSmallRows : 1], tail_s[SMALL ? kSmallRows : 1];
-  RemapWs ws = global;
-  if constexpr (SMALL) {
-    ws.bits = bits_s;
-    ws.first = first_s;
-    ws.rows = rows_s;
-    ws.need = need_s;
-    ws.tail = tail_s;
-  }
   griddep_wait();
   griddep_launch_dependents();
-  const int rank = SMALL ? 0 : (int)cg::this_cluster().block_rank(), ncta = SMALL ? 1 : (int)cg::this_cluster().num_blocks();
-  auto sync = [] {
-    if constexpr (SMALL) __syncthreads();
-    else cg::this_cluster().sync();
-  };
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ncta = (int)cluster.num_blocks();
   const int t = threadIdx.x, lane = t & 31;
   const int64_t th = (int64_t)rank * kMapThreads + t, nth = (int64_t)ncta * kMapThreads;
   const int64_t wp = th >> 5, nwp = nth >> 5;
@@ -165,7 +152,7 @@ __global__ void __launch_bounds__(kMapThreads)
     ws.copies[b] = make_int4(0, 0, 0, 0);
     lens_out[b] = (int32_t)held;
   }
-  sync();
+  cluster.sync();
   // whole pages are shared as they are
   for (int64_t b = wp; b < g.batch; b += nwp) {
     const int4 r = ws.rows[b];
@@ -183,13 +170,13 @@ __global__ void __launch_bounds__(kMapThreads)
       table_out[b * g.max_pages + i] = page;
     }
   }
-  sync();
+  cluster.sync();
   // owners of part-filled pages
   for (int64_t b = th; b < g.batch; b += nth) {
     const int tail = ws.tail[b];
     if (tail >= 0) atomicMin(&ws.owner[tail], (int32_t)b);
   }
-  sync();
+  cluster.sync();
   for (int64_t b = th; b < g.batch; b += nth) {
     const int4 r = ws.rows[b];
     const int tail = ws.tail[b];
@@ -207,12 +194,12 @@ __global__ void __launch_bounds__(kMapThreads)
     const int lost = r.z && tail < 0;
     ws.need[b] = r.w - r.y - (keeps | lost);
   }
-  sync();
+  cluster.sync();
   // ranks: every CTA counts the free pages and the wanted entries of its slice
   const int64_t w0 = words * rank / ncta, w1 = words * (rank + 1) / ncta;
   const int64_t b0 = (int64_t)g.batch * rank / ncta, b1 = (int64_t)g.batch * (rank + 1) / ncta;
   auto free_of = [&](int64_t w) {
-    uint32_t f = ~*const_cast<volatile uint32_t*>(&ws.bits[w]);
+    uint32_t f = ~__ldcg(&ws.bits[w]);
     if (w == words - 1 && (g.num_pages & 31)) f &= (1u << (g.num_pages & 31)) - 1u;
     return f;
   };
@@ -225,10 +212,10 @@ __global__ void __launch_bounds__(kMapThreads)
     cta_excl(n, wsum, &total);
     if (t == 0) part[1] = total;
   }
-  sync();
+  cluster.sync();
   int64_t free_before = 0, want_before = 0, free_all = 0, want_all = 0;
   for (int c = 0; c < ncta; ++c) {
-    const int64_t* other = SMALL ? part : cg::this_cluster().map_shared_rank(part, c);
+    const int64_t* other = cluster.map_shared_rank(part, c);
     const int64_t f = other[0], n = other[1];
     if (c < rank) {
       free_before += f;
@@ -258,7 +245,7 @@ __global__ void __launch_bounds__(kMapThreads)
     if (b < b1) ws.first[b] = at;
     want_before += total;
   }
-  sync();   // also: no CTA leaves while another reads its shared memory
+  cluster.sync();   // also: no CTA leaves while another reads its shared memory
   if (!enough) return;
   for (int64_t b = wp; b < g.batch; b += nwp) {
     const int4 r = ws.rows[b];
@@ -273,13 +260,13 @@ __global__ void __launch_bounds__(kMapThreads)
   }
 }
 
-// Copies `bytes` bytes (a multiple of any size) from src to dst, both 16-byte
-// aligned, over the CTA's threads.
-__device__ __forceinline__ void cta_copy(uint8_t* dst, const uint8_t* src, int64_t bytes) {
-  const int64_t n = bytes / 16;
-  for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
+// Copies `bytes` bytes from src to dst, both 16-byte aligned: thread t of n.
+__device__ __forceinline__ void copy_bytes(uint8_t* dst, const uint8_t* src, int64_t bytes, int t, int n) {
+  const int64_t n16 = bytes / 16;
+#pragma unroll 4
+  for (int64_t i = t; i < n16; i += n)
     reinterpret_cast<uint4*>(dst)[i] = __ldcs(reinterpret_cast<const uint4*>(src) + i);
-  for (int64_t i = n * 16 + threadIdx.x; i < bytes; i += blockDim.x) dst[i] = src[i];
+  for (int64_t i = n16 * 16 + t; i < bytes; i += n) dst[i] = src[i];
 }
 
 __global__ void __launch_bounds__(256)
@@ -297,8 +284,194 @@ __global__ void __launch_bounds__(256)
     if (!KVQ3_CHECK(status, in_range(from, g.record_bytes, g.num_pages * g.page_bytes) &&
                                 in_range(to, g.record_bytes, g.num_pages * g.page_bytes)))
       continue;
-    cta_copy(pool + to, pool + from, (int64_t)c.z * g.nb * g.sb);
-    cta_copy(pool + to + g.scale_hdr_bytes, pool + from + g.scale_hdr_bytes, (int64_t)c.z * g.cb);
+    copy_bytes(pool + to, pool + from, (int64_t)c.z * g.nb * g.sb, threadIdx.x, blockDim.x);
+    copy_bytes(pool + to + g.scale_hdr_bytes, pool + from + g.scale_hdr_bytes, (int64_t)c.z * g.cb, threadIdx.x, blockDim.x);
+  }
+}
+
+// The whole remap of a small table, by every CTA for itself: the first CTA
+// writes the new table and lengths, all copy.
+__global__ void __launch_bounds__(kMapThreads)
+    remap_small_kernel(const __grid_constant__ CacheGeom g, uint8_t* pool, const int32_t* __restrict__ table,
+                       const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ src,
+                       const int32_t* __restrict__ new_lens, int32_t* __restrict__ table_out,
+                       int32_t* __restrict__ lens_out, int32_t* status) {
+  __shared__ uint32_t bits[kSmallPages / 32];        // pages held by the new table
+  __shared__ uint32_t free_before[kSmallPages / 32]; // free pages before each word
+  __shared__ int4 rows[kSmallRows];                  // source row, then: keeps its part-filled page; whole pages; tokens
+                                                     // of the part-filled one; entries
+  __shared__ int32_t tail[kSmallRows];               // the part-filled page, -1 where there is none
+  __shared__ uint32_t first[kSmallRows];             // entries from the free pages, then the rank of the first
+  __shared__ int32_t copy_from[kSmallRows], copy_to[kSmallRows];
+  __shared__ uint32_t copy_tokens[kSmallRows];
+  __shared__ unsigned long long wsum[kMapThreads / 32];
+  __shared__ uint32_t n_copies;
+  const int t = threadIdx.x, lane = t & 31, wid = t >> 5;
+  const int words = (int)((g.num_pages + 31) / 32), batch = g.batch;
+  for (int i = t; i < words; i += kMapThreads) bits[i] = 0;
+  if (t == 0) n_copies = 0;
+  griddep_wait();
+  griddep_launch_dependents();
+  const bool lead = blockIdx.x == 0;
+  int32_t* st = lead ? status : nullptr;
+  const int P = g.page_size;
+  const int64_t cap = (int64_t)g.max_pages * P;
+  if (t < batch) {
+    const int s = src[t];
+    const int64_t want = new_lens[t];
+    const int64_t len = s >= 0 && s < batch ? seq_lens[s] : 0;
+    int64_t held = 0, entries = 0;
+    int from = -1;
+    if (s < -1 || s >= batch) {
+      set_status(st, KVQ3_DEV_BAD_SEQ);
+    } else if (want < 0 || want > cap || len < 0 || len > cap) {
+      set_status(st, KVQ3_DEV_BAD_LEN);
+    } else {
+      from = s;
+      held = min(len, want);
+      entries = (want + P - 1) / P;
+    }
+    const int full = (int)(held / P), rest = (int)(held % P);
+    int page = -1;
+    if (rest) {
+      page = table[(int64_t)from * g.max_pages + full];
+      if (page < 0 || page >= g.num_pages) {
+        set_status(st, KVQ3_DEV_BAD_PAGE);
+        page = -1;
+      }
+    }
+    rows[t] = make_int4(from, full, rest, (int)entries);
+    tail[t] = page;
+    if (lead) lens_out[t] = (int32_t)held;
+  }
+  __syncthreads();
+  // whole pages are shared as they are
+  for (int b = wid; b < batch; b += kMapThreads / 32) {
+    const int4 r = rows[b];
+    const int end = lead ? g.max_pages : r.y;
+    for (int i = lane; i < end; i += 32) {
+      int32_t page = -1;
+      if (i < r.y) {
+        page = table[(int64_t)r.x * g.max_pages + i];
+        if (page < 0 || page >= g.num_pages) {
+          set_status(st, KVQ3_DEV_BAD_PAGE);
+          page = -1;
+        } else {
+          atomicOr(&bits[page >> 5], 1u << (page & 31));
+        }
+      }
+      if (lead) table_out[(int64_t)b * g.max_pages + i] = page;
+    }
+  }
+  __syncthreads();
+  // a part-filled page stays with the lowest row that has it, unless some row shares it whole
+  for (int b = wid; b < batch; b += kMapThreads / 32) {
+    const int page = tail[b];
+    bool lower = false;
+    if (page >= 0)
+      for (int c = lane; c < b; c += 32) lower |= tail[c] == page;
+    lower = __any_sync(kFull, lower);
+    if (lane == 0) {
+      const bool keeps = page >= 0 && !lower && !((bits[page >> 5] >> (page & 31)) & 1u);
+      const int4 r = rows[b];
+      rows[b].x = keeps;
+      first[b] = (uint32_t)(r.w - r.y - (keeps || (r.z && page < 0) ? 1 : 0));   // an unreadable one keeps its -1
+    }
+  }
+  __syncthreads();
+  const bool keeps = t < batch && rows[t].x;
+  const uint32_t need = t < batch ? first[t] : 0;
+  if (keeps) {
+    atomicOr(&bits[tail[t] >> 5], 1u << (tail[t] & 31));
+    if (lead) table_out[(int64_t)t * g.max_pages + rows[t].y] = tail[t];
+  }
+  __syncthreads();
+  // ranks of the free pages and of the wanted entries, in one sum
+  constexpr int WPT = kSmallPages / 32 / kMapThreads;
+  uint32_t mine[WPT], free_here = 0;
+#pragma unroll
+  for (int i = 0; i < WPT; ++i) {
+    const int w = t * WPT + i;
+    uint32_t f = w < words ? ~bits[w] : 0u;
+    if (w == words - 1 && (g.num_pages & 31)) f &= (1u << (g.num_pages & 31)) - 1u;
+    mine[i] = __popc(f);
+    free_here += mine[i];
+  }
+  const unsigned long long v = ((unsigned long long)free_here << 32) | need;
+  unsigned long long incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long x = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += x;
+  }
+  if (lane == 31) wsum[wid] = incl;
+  __syncthreads();
+  unsigned long long before = incl - v, total = 0;
+#pragma unroll
+  for (int w = 0; w < kMapThreads / 32; ++w) {
+    before += w < wid ? wsum[w] : 0;
+    total += wsum[w];
+  }
+  uint32_t at = (uint32_t)(before >> 32);
+#pragma unroll
+  for (int i = 0; i < WPT; ++i) {
+    if (t * WPT + i < words) free_before[t * WPT + i] = at;
+    at += mine[i];
+  }
+  if (t < batch) first[t] = (uint32_t)before;
+  if ((uint32_t)total > (uint32_t)(total >> 32)) {   // fewer free pages than wanted: nothing is copied
+    if (t == 0) set_status(st, KVQ3_DEV_NO_PAGE);
+    return;
+  }
+  __syncthreads();
+  // the free page of a rank
+  auto free_page = [&](uint32_t rank) {
+    int lo = 0, hi = words - 1;
+    while (lo < hi) {   // the last word with at most `rank` free pages before it
+      const int m = (lo + hi + 1) >> 1;
+      if (free_before[m] <= rank) lo = m;
+      else hi = m - 1;
+    }
+    uint32_t f = ~bits[lo];
+    for (uint32_t k = rank - free_before[lo]; k > 0; --k) f &= f - 1;
+    return lo * 32 + __ffs(f) - 1;
+  };
+  if (t < batch && tail[t] >= 0 && !keeps) {
+    const uint32_t k = atomicAdd(&n_copies, 1u);   // in any order: the copies are independent
+    copy_from[k] = tail[t];
+    copy_to[k] = free_page(first[t]);
+    copy_tokens[k] = rows[t].z;
+  }
+  if (lead) {
+    for (int b = wid; b < batch; b += kMapThreads / 32) {
+      const int4 r = rows[b];
+      const uint32_t at0 = first[b];
+      const int start = r.y + (r.x || (r.z && tail[b] < 0) ? 1 : 0);
+      for (int i = start + lane; i < r.w; i += 32)
+        table_out[(int64_t)b * g.max_pages + i] = free_page(at0 + (uint32_t)(i - start));
+    }
+  }
+  __syncthreads();
+  // a warp copies the scales of a record's slots in use, or a quarter of their
+  // codes: a few accesses a lane, all under way together
+  const int recs = 2 * g.hkv;
+  const int64_t items = (int64_t)n_copies * recs * kCopyPieces;
+  for (int64_t it = (int64_t)wid * gridDim.x + blockIdx.x; it < items; it += (int64_t)gridDim.x * (kMapThreads / 32)) {
+    const int64_t whole = it / kCopyPieces;
+    const int piece = (int)(it - whole * kCopyPieces), c = (int)(whole / recs);
+    const int64_t rec = (whole - (int64_t)c * recs) * g.record_bytes;
+    const int64_t from = copy_from[c] * g.page_bytes + rec, to = copy_to[c] * g.page_bytes + rec;
+    if (!KVQ3_CHECK(status, in_range(from, g.record_bytes, g.num_pages * g.page_bytes) &&
+                                in_range(to, g.record_bytes, g.num_pages * g.page_bytes)))
+      continue;
+    if (piece == kCopyPieces - 1) {
+      copy_bytes(pool + to, pool + from, (int64_t)copy_tokens[c] * g.nb * g.sb, lane, 32);
+    } else {
+      const int64_t bytes = (int64_t)copy_tokens[c] * g.cb;
+      const int64_t part = (bytes / 16 + kCopyPieces - 2) / (kCopyPieces - 1) * 16;
+      const int64_t b0 = min(bytes, piece * part), b1 = piece == kCopyPieces - 2 ? bytes : min(bytes, b0 + part);
+      copy_bytes(pool + to + g.scale_hdr_bytes + b0, pool + from + g.scale_hdr_bytes + b0, b1 - b0, lane, 32);
+    }
   }
 }
 
@@ -472,37 +645,44 @@ kvq3_status kvq3_remap(const kvq3_cache_desc* desc, const kvq3_cache* cache, con
   if (s != KVQ3_OK) return s;
   if ((s = check_cache(g, cache, true)) != KVQ3_OK) return s;
   if (!cache->page_table || !src || !new_lens || !table_out || !lens_out) return KVQ3_ERR_INVALID_ARG;
-  // the old table and lengths are read while the new ones are written
-  auto apart = [](const int32_t* a, const int32_t* b, int64_t n) {
-    return reinterpret_cast<uintptr_t>(a) + n * 4 <= reinterpret_cast<uintptr_t>(b) ||
-           reinterpret_cast<uintptr_t>(b) + n * 4 <= reinterpret_cast<uintptr_t>(a);
+  // the inputs are read while the outputs are written
+  auto apart = [](const int32_t* a, int64_t na, const int32_t* b, int64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x + na * 4 <= y || y + nb * 4 <= x;
   };
-  if (!apart(table_out, cache->page_table, (int64_t)g.batch * g.max_pages) || !apart(lens_out, cache->seq_lens, g.batch))
+  const int64_t n = g.batch, cells = (int64_t)g.batch * g.max_pages;
+  for (const int32_t* in : {cache->seq_lens, src, new_lens})
+    if (!apart(lens_out, n, in, n) || !apart(table_out, cells, in, n)) return KVQ3_ERR_INVALID_ARG;
+  if (!apart(lens_out, n, cache->page_table, cells) || !apart(table_out, cells, cache->page_table, cells) ||
+      !apart(table_out, cells, lens_out, n))
     return KVQ3_ERR_INVALID_ARG;
   if (g.num_pages >= ((int64_t)1 << 31)) return KVQ3_ERR_UNSUPPORTED;
   const RemapWs ws = remap_layout(g, workspace);
   if (!workspace || ws_bytes < ws.bytes || reinterpret_cast<uintptr_t>(workspace) % 256) return KVQ3_ERR_WORKSPACE;
-  const bool small = g.batch <= kSmallRows && (int64_t)g.batch * g.max_pages <= kSmallEntries && g.num_pages <= kSmallPages;
-  const unsigned ctas = small ? 1 : kMapCluster;
+  const int64_t copies = (int64_t)g.batch * 2 * g.hkv;   // records that may be copied
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.x = kMapCluster;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kMapThreads);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
-  cfg.numAttrs = small ? 1 : 2;
-  auto run = [&](auto kernel) {
-    return cudaLaunchKernelEx(&cfg, kernel, g, cache->page_table, cache->seq_lens, src, new_lens, table_out, lens_out, ws,
-                              dev_status);
-  };
-  if ((small ? run(remap_kernel<true>) : run(remap_kernel<false>)) != cudaSuccess) return KVQ3_ERR_CUDA;
-  const int64_t items = (int64_t)g.batch * 2 * g.hkv, cap = (int64_t)sm_count() * 8;
-  cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, std::min(items, cap)));
+  if (g.batch <= kSmallRows && (int64_t)g.batch * g.max_pages <= kSmallEntries && g.num_pages <= kSmallPages) {
+    cfg.gridDim = dim3((unsigned)std::min<int64_t>(std::max(1, sm_count()), (copies * kCopyPieces + 31) / 32));
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, remap_small_kernel, g, static_cast<uint8_t*>(cache->pool),
+                                          cache->page_table, cache->seq_lens, src, new_lens, table_out, lens_out,
+                                          dev_status));
+  }
+  cfg.gridDim = dim3(kMapCluster);
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, remap_kernel, g, cache->page_table, cache->seq_lens, src, new_lens, table_out, lens_out, ws,
+                         dev_status) != cudaSuccess)
+    return KVQ3_ERR_CUDA;
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(copies, (int64_t)std::max(1, sm_count()) * 8));
   cfg.blockDim = dim3(256);
   cfg.numAttrs = 1;
   return cuda_status(cudaLaunchKernelEx(&cfg, remap_copy_kernel, g, static_cast<uint8_t*>(cache->pool),

@@ -536,9 +536,9 @@ kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc *des
  *     A page is free when no row of the new table holds it: there is no other
  *     allocation state, and a page held outside the table (a kept prefix)
  *     is one that some row of the batch holds.
- * table_out: device int32 [batch][max_pages_per_seq], apart from the cache's
- * table (KVQ3_ERR_INVALID_ARG), -1 past new_lens[b]; lens_out: device int32
- * [batch] = held, apart from the cache's lengths.  The caller then uses the two in
+ * table_out: device int32 [batch][max_pages_per_seq], -1 past new_lens[b];
+ * lens_out: device int32 [batch] = held.  Neither may overlap the other or an
+ * input (KVQ3_ERR_INVALID_ARG).  The caller then uses the two in
  * place of the cache's page_table and seq_lens.  Contents of a page beyond
  * the tokens it held are left as they were; key bounds of a copied page are
  * not copied (kvq3_key_bounds makes them).

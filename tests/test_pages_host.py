@@ -89,12 +89,16 @@ def test_remap_refusals_and_workspace(K):
     assert need == up(4 * -(-n // 32)) + 2 * up(4 * n) + 2 * up(4 * b) + up(8 * b) + 2 * up(16 * b)
     table, lens = ctypes.c_void_p(8192), ctypes.c_void_p(12288)
 
-    def call(src=A, new=B, table_out=C, lens_out=A, ws=A, n_ws=need, desc=d, cache=None):
+    D, E = ctypes.c_void_p(1 << 23), ctypes.c_void_p(1 << 24)
+
+    def call(src=A, new=B, table_out=C, lens_out=D, ws=E, n_ws=need, desc=d, cache=None):
         return K.lib.kvq3_remap(ctypes.byref(desc), ctypes.byref(cache or _cache(K)), src, new, table_out, lens_out, ws,
                                 n_ws, None, None)
     for kw in (dict(src=None), dict(new=None), dict(table_out=None), dict(lens_out=None), dict(table_out=table),
                dict(table_out=ctypes.c_void_p(8192 + 44)), dict(table_out=ctypes.c_void_p(8192 - 4)),
-               dict(lens_out=lens), dict(lens_out=ctypes.c_void_p(12288 + 8)), dict(cache=_cache(K, table=None)), dict(cache=_cache(K, lens=None))):
+               dict(lens_out=lens), dict(lens_out=ctypes.c_void_p(12288 + 8)),
+               dict(lens_out=A), dict(lens_out=B), dict(table_out=A), dict(table_out=ctypes.c_void_p((1 << 21) - 4)),
+               dict(lens_out=ctypes.c_void_p((1 << 22) + 40)), dict(lens_out=table), dict(cache=_cache(K, table=None)), dict(cache=_cache(K, lens=None))):
         assert call(**kw) == INVALID, kw
     for kw in (dict(ws=None), dict(n_ws=need - 1), dict(ws=ctypes.c_void_p(264))):
         assert call(**kw) == WORKSPACE, kw
