@@ -14,10 +14,19 @@
 // below what a page ranking resolves, at half the bytes of fp32.
 //
 // One lane owns 32 coordinates of a (page, kv head) and walks the page's
-// tokens, so the minima and maxima stay in registers and nothing is reduced
-// across lanes when there are pages enough to fill the GPU; with few pages
-// (the append of a decode step) 2 to 16 lanes share a page's tokens and meet
-// by shuffles.
+// tokens, two batches of four in flight in turn, so the minima and maxima stay
+// in registers; 2 to 16 lanes share a page's tokens and meet by shuffles where
+// that fills the GPU (the append of a decode step, the last round over a long
+// prompt).  What bounds it is the unpacking: per 32 coordinates of a token 32
+// packed minima and maxima, 16 masks and about 12 shifts on the half-rate
+// integer pipe (70 % busy) and 32 half2 products on another half-rate one.
+// 16 sequences of 32K tokens (8 kv heads of 128, 3-bit codes, 128-token pages):
+// 87 us, 2.7 TB/s of 235 MB.  Runs of consecutive tokens per lane (constant
+// address steps) took 95 us (one 48-byte piece per memory wavefront), window
+// tables with 5 kinds of field position instead of 8 84 to 88.
+#include <algorithm>
+#include <atomic>
+
 #include "kvq3_decode.cuh"
 
 using namespace kvq3;
@@ -367,13 +376,17 @@ __global__ void __launch_bounds__(kThreads)
 template <int NBIT, int SCALE>
 cudaError_t launch_bounds(const CacheGeom& g, const kvq3_cache* c, const int32_t* first, __half* bounds, int32_t* st,
                           cudaStream_t stream) {
-  static int per_sm = 0;   // resident CTAs (the same on every sm_103a device)
-  if (per_sm == 0 &&
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, key_bounds_kernel<NBIT, SCALE>, kThreads, 0) != cudaSuccess)
-    return cudaErrorUnknown;
-  const int64_t most = ((int64_t)g.batch * g.max_pages * g.hkv * g.d + kThreads - 1) / kThreads;   // a lane per 32 x 1/32
-  int64_t blocks = (int64_t)sm_count() * (per_sm > 0 ? per_sm : 1);
-  if (blocks > most) blocks = most;
+  static std::atomic<int> resident{0};   // CTAs per SM (the same on every sm_103a device)
+  int per_sm = resident.load(std::memory_order_relaxed);
+  if (per_sm == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, key_bounds_kernel<NBIT, SCALE>, kThreads, 0) != cudaSuccess)
+      return cudaErrorUnknown;
+    resident.store(per_sm, std::memory_order_relaxed);
+  }
+  // no more CTAs than a lane for each coordinate of each page that the cache's tables can name
+  const double most = (double)g.batch * g.max_pages * g.hkv * g.d / kThreads + 1.0;
+  int64_t blocks = (int64_t)sm_count() * std::max(1, per_sm);
+  if ((double)blocks > most) blocks = (int64_t)most;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

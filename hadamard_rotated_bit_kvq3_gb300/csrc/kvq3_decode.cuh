@@ -41,6 +41,24 @@
 //    value scales, at up to 4 heads per kv head and in the asymmetric
 //    variant.  Per-(token, block) scales multiply the per-block partial dot
 //    products (keys) or the probabilities (values).
+//
+// Attention over selected pages (template flag SEL; kvq3_decode_attn_pages)
+// keeps the ring, the steps and their arithmetic, and replaces what surrounds
+// them: one cluster of CTAs per (sequence, kv head) instead of ranges of a
+// flattened list, the list's entries instead of the page table's order, and a
+// merge in the cluster's shared memory instead of partials and a second
+// kernel.  A decode step of this kind is short (4,096 tokens of each of 128
+// units are 54 MB, 8 us at the HBM rate), so the latency around the loop
+// counts: count, length, list and query are read at once, the first chunk of
+// every CTA is asked for before the second of any, the query's fragments are
+// built in shares, and the merge has every load under way before its first
+// use.  Measured on 16 sequences x 8 kv heads, G = 4, d = 128, 4,096 tokens
+// each: 39.6 us with the flattened list and second kernel, 27.8 as clusters,
+// 24.6 now (2.2 TB/s); 8 x 8, G = 8, E4M3 scales, 16,384 tokens: 65 to 50.2 us
+// (2.1 TB/s); 64 x 4, d = 256, 16-token pages, 2,048 tokens: 84 to 60 us (1.8
+// TB/s).  What is left above the loop's own issue rate (1.14 us a 256-token
+// chunk and SM): about 6.5 us to start and merge, and SMs that hold 4 CTAs
+// while others hold 3.
 #pragma once
 
 #include <float.h>

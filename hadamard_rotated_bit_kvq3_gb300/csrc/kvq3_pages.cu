@@ -19,12 +19,18 @@
 // waiting for another.  A larger table is a thread-block cluster's work, its
 // state in the workspace and the hardware cluster barrier between, and the
 // copies, the only bulk traffic, are a second kernel's, its programmatic
-// dependent.  Only the slots in use are copied.
+// dependent.  Only the slots in use are copied.  16 sequences that grow by a
+// token: 5.0 us; 64 sequences in beams of 8, a third of them with a page to
+// copy (2.3 MB): 8.4 us (13.4 and 18.1 as a cluster with a copy kernel).
 //
 // Compaction is a gather of packed vectors (codes and scales as stored); one
 // CTA takes a run of kept tokens of a (sequence, kv head), resolves each
 // token's record addresses once into shared memory, and moves the code strings
-// and scale headers with the widest accesses their sizes allow.
+// and scale headers with the widest accesses their sizes allow, every load
+// under way before the first store.  Bound by HBM sectors: a kept token at
+// random reads 48 + 4 bytes per vector but touches about 104 (whole 32-byte
+// sectors).  16 x 8 heads, 4,096 of 16,384 tokens kept: 31.4 us, 3.5 TB/s of
+// the bytes moved, 5.2 TB/s of sectors (35.6 us with one access at a time).
 #include <cooperative_groups.h>
 
 #include <algorithm>

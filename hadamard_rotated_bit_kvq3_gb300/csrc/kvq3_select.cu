@@ -9,13 +9,21 @@
 // (each lane loads 16 consecutive bytes of a page's row; the columns of K are
 // taken in that order on both sides) and the query parts as B, split into
 // hi + lo fp16 halves (two columns per head), so the scores carry about fp32
-// accuracy.  Bound by HBM: 4d bytes per (page, kv head) for 4 d G flops.
+// accuracy.  Bound by HBM: 4d bytes per (page, kv head) for 4 d G flops.  Each
+// row's registers are refilled as they are used, so 8 KB a warp stay in
+// flight.  64 sequences of up to 64K tokens, 4 kv heads of 256, 16-token pages
+// (549 MB of bounds): 99 us, 5.5 TB/s, 82 % of the measured copy rate (123 us
+// with a CTA per tile, loading, then computing).  16 sequences of 32K, 8 kv
+// heads of 128, 128-token pages (17 MB): 5.9 us, latency.
 //
 // Selection.  One CTA per (sequence, kv head): the scores as order-preserving
 // 32-bit keys (in registers up to 8,192 pages), a histogram search for the
 // budget-th largest between the forced first and last pages, and one ordered
 // compaction by ballots that breaks ties towards the lower page.  Bound by
-// latency, a few block barriers of a row of a few thousand keys; no sort.
+// latency, a few block barriers of a row of a few thousand keys; no sort.  256
+// rows of up to 4,096 pages, 256 of them chosen: 7.3 us (14.4 with three radix
+// passes over keys in shared memory, 11.8 with the keys in registers); 128 rows
+// of 256 pages: 3.5 us.
 #include <math.h>
 
 #include "kvq3_internal.h"

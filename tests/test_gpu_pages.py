@@ -318,6 +318,8 @@ ATTN = [
     (dict(lens=(33000, 0, 17), page=16, hkv=1, scale="e4m3zp", d=64, block=32), 3, 2000),
     # long lists of several units: whole clusters, chunks in turn
     (dict(lens=(9000, 8000, 100, 0), page=32, hkv=4, bits=4), 6, 250),
+    # pages larger than a chunk; as large as the copy stages take
+    (dict(lens=(700, 300), page=256, hkv=2), 4, 3), (dict(lens=(2500, 1024), page=1024, hkv=1), 4, 2),
 ]
 
 
@@ -392,6 +394,69 @@ def test_decode_attn_pages_wait_that_runs_out(kw, G, row):
         c.status.zero_()
     _near(_attend(c, q, pages, counts), PO.decode_pages(c.pool, c.layout, c.U, q, c.lens, c.table, pages, counts))
     assert c.flags() == 0
+
+
+def test_decode_attn_pages_refuses_pages_past_the_stages():
+    c = Pages(lens=(100,), page=4096, hkv=1)
+    q, (pages, counts) = c.queries(4), _lists(c, 1)
+    with pytest.raises(c.K.Kvq3Error) as e:
+        _attend(c, q, pages, counts)
+    assert e.value.status == 2                   # as the dense decode: two stages of a page do not fit
+
+
+def test_offsets_past_32_bits():
+    # the same cache at the end of a 6.4 GB pool: every operator gives the same bits
+    page, hkv, d, far = 128, 8, 128, 60000
+    c = Pages(lens=(700, 333, 0, 0), page=page, hkv=hkv, maxp=7, spare=8, d=d)
+    t, K, L = c.torch, c.K, c.layout
+    free = t.cuda.mem_get_info()[0]
+    assert far * L.page_bytes > 1 << 32
+    if free < 2 * far * L.page_bytes:
+        pytest.skip("not enough device memory")
+    q, G = c.queries(4), 4
+    pages, counts = _lists(c, 5)
+    keep = c.rng.integers(0, 333, (1, hkv, 300)).astype(np.int32)
+
+    def run(shift):
+        n = c.N + shift
+        pool = t.zeros(n * L.page_bytes, dtype=t.uint8, device="cuda")
+        pool[shift * L.page_bytes:] = c.dev(c.pool)
+        table = c.dev(np.where(c.table >= 0, c.table + shift, -1).astype(np.int32))
+        lens = c.dev(c.lens)
+        desc = K.CacheDesc(d, hkv, 64, 3, 1, 1e-6, page, c.B, c.maxp, 0, n)
+        cache = K.Cache(pool.data_ptr(), table.data_ptr(), lens.data_ptr())
+        bounds = t.zeros(n, hkv, 2, d, dtype=t.float16, device="cuda")
+        scores = t.empty(c.B, hkv, c.maxp, device="cuda")
+        out = t.empty(c.B, hkv * G, d, dtype=t.float16, device="cuda")
+        K.kvq3_key_bounds(desc, cache, None, bounds, c.status)
+        K.kvq3_page_scores(c.rot.handle, desc, cache, bounds, c.dev(q), scores, c.status)
+        K.kvq3_decode_attn_pages(c.rot.handle, desc, cache, c.dev(q), c.dev(pages), c.dev(counts), out, 0.0, c.status)
+        # row 2 gets pages for 300 tokens gathered from row 1 (by hand: the pages below `shift` are free too)
+        table2 = table.clone()
+        spare = np.setdiff1d(np.arange(c.N), c.table[c.table >= 0])
+        table2[2, :3] = c.dev((spare[:3] + shift).astype(np.int32))
+        cache2 = K.Cache(pool.data_ptr(), table2.data_ptr(), lens.data_ptr())
+        i32 = lambda x: c.dev(np.array(x, np.int32))   # noqa: E731
+        K.kvq3_compact(desc, cache2, i32([1]), i32([2]), c.dev(keep), i32([300]), c.status)
+        t.cuda.synchronize()
+        moved = pool[shift * L.page_bytes:].cpu().numpy()
+        got = (bounds[shift:].cpu().numpy().view(np.uint16), scores.cpu().numpy(), out.cpu().numpy(), moved)
+        # a fork whose part-filled page lies past 4 GB is copied into the lowest free page
+        table3, lens3 = t.empty_like(table), t.empty_like(lens)
+        ws = t.empty(K.kvq3_remap_workspace_size(desc), dtype=t.uint8, device="cuda")
+        K.kvq3_remap(desc, cache, i32([0, 1, -1, 0]), i32([700, 333, 0, 700]), table3, lens3, ws, c.status)
+        t.cuda.synchronize()
+        a, z = int(table3[0, 5]), int(table3[3, 5])
+        rec = pool.view(n, hkv * 2, L.record_bytes)
+        hdr, tok = page * L.nb * L.sb, 700 % page
+        assert a != z and bool((rec[a, :, :tok * L.nb * L.sb] == rec[z, :, :tok * L.nb * L.sb]).all())
+        assert bool((rec[a, :, hdr:hdr + tok * L.code_bytes] == rec[z, :, hdr:hdr + tok * L.code_bytes]).all())
+        return got
+
+    near, past = run(0), run(far)
+    assert c.flags() == 0
+    for a, b in zip(near, past):
+        assert np.array_equal(a, b)
 
 
 def test_decode_attn_pages_is_deterministic():
