@@ -348,10 +348,11 @@ def _refuse(t, name: str, dtype, shape, where: str):
 
 def _at(t, name: str, dtype, shape, where: str) -> int:
     """Address of a tensor that is as the call needs it."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() < 0 \
-            or t.get_device() != _torch()._C._cuda_getDevice():
-        _refuse(t, name, dtype, shape, where)
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        d = t.get_device()   # -1: not a CUDA tensor
+        if d >= 0 and d == _torch()._C._cuda_getDevice():
+            return t.data_ptr()
+    _refuse(t, name, dtype, shape, where)
 
 
 _torch_module = None
