@@ -246,17 +246,19 @@ def _library(s):
         rot = K.kvq3_rotation_create_from_params(c["d"], s["signs"].cpu().numpy(), s["quats"].cpu().numpy())
     if c["op"] == "remap":
         ws = torch.empty(K.kvq3_remap_workspace_size(desc), dtype=torch.uint8, device=DEV)
-    return K, desc, cache, rot, ws
+    # what a pass returns: the pages that the cache knows, without the spare one behind them
+    whole = s["bounds"][: s["num_pages"]] if c["op"] == "bounds" else s["pool"][: s["num_pages"]]
+    return K, desc, cache, rot, ws, whole
 
 
 def _run_own(s):
     if "library" not in s:
         s["library"] = _library(s)
-    K, desc, cache, rot, ws = s["library"]
+    K, desc, cache, rot, ws, whole = s["library"]
     c, op = s["case"], s["case"]["op"]
     if op == "bounds":
         K.kvq3_key_bounds(desc, cache, s["first"], s["bounds"], s["status"])
-        return s["bounds"][: s["num_pages"]]
+        return whole
     if op == "scores":
         K.kvq3_page_scores(rot, desc, cache, s["bounds"], s["q"], s["scores"], s["status"])
         return s["scores"]
@@ -269,9 +271,9 @@ def _run_own(s):
         return s["out"]
     if op == "remap":
         K.kvq3_remap(desc, cache, s["src"], s["new_lens"], s["table_out"], s["lens_out"], ws, s["status"])
-        return s["table_out"], s["lens_out"], s["pool"][: s["num_pages"]]
+        return s["table_out"], s["lens_out"], whole
     K.kvq3_compact(desc, cache, s["src_seq"], s["dst_seq"], s["keep"], s["n_keep"], s["status"])
-    return s["pool"][: s["num_pages"]]
+    return whole
 
 
 # ---------------------------------------------------------------- the plain forms
