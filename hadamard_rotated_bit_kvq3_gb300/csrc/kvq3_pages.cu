@@ -311,11 +311,9 @@ __global__ void __launch_bounds__(kMapThreads)
   __shared__ int32_t copy_from[kSmallRows], copy_to[kSmallRows];
   __shared__ uint32_t copy_tokens[kSmallRows];
   __shared__ unsigned long long wsum[kMapThreads / 32];
-  __shared__ uint32_t n_copies;
   const int t = threadIdx.x, lane = t & 31, wid = t >> 5;
   const int words = (int)((g.num_pages + 31) / 32), batch = g.batch;
   for (int i = t; i < words; i += kMapThreads) bits[i] = 0;
-  if (t == 0) n_copies = 0;
   griddep_wait();
   griddep_launch_dependents();
   const bool lead = blockIdx.x == 0;
@@ -385,14 +383,16 @@ __global__ void __launch_bounds__(kMapThreads)
     }
   }
   __syncthreads();
-  const bool keeps = t < batch && rows[t].x;
+  const bool keeps = t < batch && rows[t].x, copies = t < batch && tail[t] >= 0 && !keeps;
   const uint32_t need = t < batch ? first[t] : 0;
   if (keeps) {
     atomicOr(&bits[tail[t] >> 5], 1u << (tail[t] & 31));
     if (lead) table_out[(int64_t)t * g.max_pages + rows[t].y] = tail[t];
   }
   __syncthreads();
-  // ranks of the free pages and of the wanted entries, in one sum
+  // ranks of the free pages, the wanted entries and the copies (the same in
+  // every CTA: each takes its share of the copies by rank), in one sum of
+  // three fields: at most 2^16 free pages, 2^16 entries, 2^9 copies
   constexpr int WPT = kSmallPages / 32 / kMapThreads;
   uint32_t mine[WPT], free_here = 0;
 #pragma unroll
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kMapThreads)
     mine[i] = __popc(f);
     free_here += mine[i];
   }
-  const unsigned long long v = ((unsigned long long)free_here << 32) | need;
+  const unsigned long long v = ((unsigned long long)free_here << 40) | ((unsigned long long)need << 16) | (copies ? 1 : 0);
   unsigned long long incl = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -418,14 +418,16 @@ __global__ void __launch_bounds__(kMapThreads)
     before += w < wid ? wsum[w] : 0;
     total += wsum[w];
   }
-  uint32_t at = (uint32_t)(before >> 32);
+  static_assert(kSmallEntries < (1 << 24) && kSmallRows < (1 << 16) && kSmallPages < (1 << 24), "fields of the sum");
+  const uint32_t want_all = (uint32_t)(total >> 16) & 0xffffffu, n_copies = (uint32_t)total & 0xffffu;
+  uint32_t at = (uint32_t)(before >> 40);
 #pragma unroll
   for (int i = 0; i < WPT; ++i) {
     if (t * WPT + i < words) free_before[t * WPT + i] = at;
     at += mine[i];
   }
-  if (t < batch) first[t] = (uint32_t)before;
-  if ((uint32_t)total > (uint32_t)(total >> 32)) {   // fewer free pages than wanted: nothing is copied
+  if (t < batch) first[t] = (uint32_t)(before >> 16) & 0xffffffu;
+  if (want_all > (uint32_t)(total >> 40)) {   // fewer free pages than wanted: nothing is copied
     if (t == 0) set_status(st, KVQ3_DEV_NO_PAGE);
     return;
   }
@@ -442,8 +444,8 @@ __global__ void __launch_bounds__(kMapThreads)
     for (uint32_t k = rank - free_before[lo]; k > 0; --k) f &= f - 1;
     return lo * 32 + __ffs(f) - 1;
   };
-  if (t < batch && tail[t] >= 0 && !keeps) {
-    const uint32_t k = atomicAdd(&n_copies, 1u);   // in any order: the copies are independent
+  if (copies) {
+    const uint32_t k = (uint32_t)before & 0xffffu;
     copy_from[k] = tail[t];
     copy_to[k] = free_page(first[t]);
     copy_tokens[k] = rows[t].z;

@@ -517,6 +517,16 @@ def test_remap_steps(kw):
     assert c.flags() == 0 and (c.table == -1).all()
 
 
+@pytest.mark.parametrize("rows", [33, 300, 512])
+def test_remap_copies_of_many_rows(rows):
+    # beams of 5, most rows with a part-filled page to copy: every CTA has to take its own share of the same list
+    rng = np.random.default_rng(rows)
+    c = Pages(d=128, hkv=1, block=32, scale="e4m3zp", page=48, lens=rng.integers(1, 300, rows), maxp=8, spare=2 * rows)
+    src = np.minimum(np.arange(rows) // 5 * 5 + rng.integers(0, 5, rows), rows - 1)
+    assert _remap(c, src, c.lens[src] + 1) and c.flags() == 0
+    assert _remap(c, np.zeros(rows), np.full(rows, c.lens[0] + 1)) and c.flags() == 0
+
+
 def test_remap_large():
     # more pages and rows than one pass of the cluster's threads
     rng = np.random.default_rng(23)
