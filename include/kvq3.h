@@ -140,7 +140,8 @@ extern "C" {
 #endif
 
 #define KVQ3_ABI_VERSION 3   /* 2: code widths 2-4, the asymmetric scale type, calibration;
-                                3: two-quaternion SO(4) blocks (KVQ3_ROT_SO4_PAIR) */
+                                3: two-quaternion SO(4) blocks (KVQ3_ROT_SO4_PAIR); the page
+                                operators are additions to it */
 
 typedef enum {
   KVQ3_OK = 0,
@@ -512,7 +513,9 @@ kvq3_status kvq3_page_select(const kvq3_cache_desc *desc, const kvq3_cache *cach
  * below the error bar of the attention); both 16-byte aligned.  No workspace:
  * one launch, whose partial results meet on chip, added in a fixed order (the
  * same call gives the same bits).  The rest as for kvq3_decode_attn;
- * KVQ3_ERR_UNSUPPORTED when batch * Hq or max_selected * P reaches 2^31. */
+ * KVQ3_ERR_UNSUPPORTED when batch * Hq or max_selected * P reaches 2^31, or
+ * when two pages of a kv head do not fit in a CTA's shared memory (as for
+ * kvq3_decode_attn). */
 kvq3_status kvq3_decode_attn_pages(kvq3_rotation rot, const kvq3_cache_desc *desc,
                                    const kvq3_cache *cache, const void *q, int32_t num_q_heads,
                                    float sm_scale, const int32_t *pages, const int32_t *counts,
