@@ -49,16 +49,17 @@
 // merge in the cluster's shared memory instead of partials and a second
 // kernel.  A decode step of this kind is short (4,096 tokens of each of 128
 // units are 54 MB, 8 us at the HBM rate), so the latency around the loop
-// counts: count, length, list and query are read at once, the first chunk of
-// every CTA is asked for before the second of any, the query's fragments are
-// built in shares, and the merge has every load under way before its first
-// use.  Measured on 16 sequences x 8 kv heads, G = 4, d = 128, 4,096 tokens
-// each: 39.6 us with the flattened list and second kernel, 27.8 as clusters,
-// 24.6 now (2.2 TB/s); 8 x 8, G = 8, E4M3 scales, 16,384 tokens: 65 to 50.2 us
-// (2.1 TB/s); 64 x 4, d = 256, 16-token pages, 2,048 tokens: 84 to 60 us (1.8
-// TB/s).  What is left above the loop's own issue rate (1.14 us a 256-token
-// chunk and SM): about 6.5 us to start and merge, and SMs that hold 4 CTAs
-// while others hold 3.
+// counts: count, length, list and query are read at once, the list's page ids
+// are looked up ahead, the first chunk of every CTA is asked for before the
+// second of any, the query's fragments are built in shares, and the merge has
+// every load under way before its first use.  Measured on 16 sequences x 8 kv
+// heads, G = 4, d = 128, 4,096 tokens each: 39.6 us with the flattened list and
+// second kernel, 27.8 as clusters, 24.5 now (2.2 TB/s); 8 x 8, G = 8, E4M3
+// scales, 16,384 tokens: 65 to 50.4 us (2.1 TB/s); 64 x 4, d = 256, 16-token
+// pages, 2,048 tokens: 84 to 59 us (1.9 TB/s).  What is left above the loop's
+// own issue rate (1.04 us a 256-token chunk and SM; 1.14 with the look-ups in
+// the refills): about 7 us to start and merge, and SMs that hold 4 CTAs while
+// others hold 3.
 #pragma once
 
 #include <float.h>
@@ -74,6 +75,7 @@ constexpr int kMaxPagesPerChunk = kChunk / 16;
 constexpr int kWarps = 4;        // consumer warps per CTA
 constexpr int kMaxStages = 8;
 constexpr int kMaxParts = 16;   // CTAs of a unit's cluster (SEL)
+constexpr int kSelPages = 256;  // listed pages that a CTA looks up ahead (SEL)
 
 struct DecodeParams {
   CacheGeom g;
@@ -571,7 +573,9 @@ __host__ __device__ constexpr bool decode_qf_smem(int D, int GPAD) { return D ==
 
 // SEL: the q1 fragments pass through shared memory in every variant (the warps
 // build them in shares), over the rotated query they are made of (the same
-// size), and the logit seeds come as a part per warp.
+// size), and the logit seeds come as a part per warp; the page ids of the
+// CTA's first kSelPages listed pages are looked up once, so that a refill
+// waits for no load (its warp holds up the others at the chunk's barrier).
 template <int D, int GPAD, bool SEL = false>
 struct DecodeSmem {
   static constexpr int kFullOff = 0;                              // kMaxStages mbarriers
@@ -582,8 +586,9 @@ struct DecodeSmem {
   static constexpr int kKofsOff = kQInvOff + GPAD * 4;            // [D/32][GPAD] logit seeds
   static constexpr int kQEnd = (kKofsOff + (SEL ? kWarps : 1) * (D / 32) * GPAD * 4 + 15) / 16 * 16;
   static constexpr int kQfOff = SEL ? kQOff : kQEnd;              // [D/16][GPAD/4][32] uint2
+  static constexpr int kPagesOff = kQEnd;                         // SEL: [kSelPages] page ids, then the cut
   static constexpr int kStageOff =
-      ((kQEnd + (!SEL && decode_qf_smem(D, GPAD) ? (D / 16) * (GPAD / 4) * 256 : 0)) + 127) / 128 * 128;
+      ((kQEnd + (SEL ? kSelPages * 4 + 16 : decode_qf_smem(D, GPAD) ? (D / 16) * (GPAD / 4) * 256 : 0)) + 127) / 128 * 128;
 };
 
 // Resident CTAs per SM the register budget is sized for: the accumulators
@@ -632,6 +637,7 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
       uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kFullOff);
       for (int s = 0; s < p.stages; ++s) mbar_init(&bars[s], 1);
       *reinterpret_cast<volatile uint32_t*>(smem + SM::kEmptyOff) = 0;
+      *reinterpret_cast<int32_t*>(smem + SM::kPagesOff + kSelPages * 4) = 0;
       fence_mbar_init();
     }
     __syncthreads();
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
   // register through the loop: the chunk descriptors carry what a refill needs.
   int sel_unit = 0, sel_b = 0, sel_kvh = 0, sel_n = 0, sel_part = 0;
   int64_t sel_seq = 0;
-  int32_t first_entry = -1;
+  int32_t my_entry = -1, my_before = -1;   // listed page number threadIdx.x of the CTA, and the one before it
   // SEL: the query rows of this warp's rounds of the rotation, EQ halves a lane
   constexpr int QR = SEL ? (GPAD + kWarps * GPWQ - 1) / (kWarps * GPWQ) : 1;
   uint4 sel_q[QR];
@@ -682,7 +688,15 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
     // everything the first copies and the query need, on its way at once
     sel_n = p.sel_counts[sel_unit];
     sel_seq = p.seq_lens[sel_b];
-    first_entry = entry_of(sel_unit, sel_part + wid * p.sel_parts);
+    {
+      const int ppc = p.pages_per_chunk, i = (int)threadIdx.x / ppc;
+      const int64_t lp = (int64_t)(sel_part + i * p.sel_parts) * ppc + ((int)threadIdx.x - i * ppc);
+      const int32_t* list = p.sel_pages + (int64_t)sel_unit * p.sel_row;
+      if (lp < p.sel_row) {
+        my_entry = list[lp];
+        if (lp > 0) my_before = list[lp - 1];
+      }
+    }
 #pragma unroll
     for (int k = 0; k < QR; ++k) {
       const int gg = (k * kWarps + wid) * GPWQ + lane / LQ;
@@ -728,7 +742,21 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
   // whole warp (lane i copies page i of the chunk): warp 0 fills the first
   // stages; afterwards the last warp to release a stage refills it
   const uint64_t pol = policy_evict_first();
-  auto issue = [&](const Cursor& c, int stage, int64_t len, int32_t entry = -1) {   // warp-collective
+  int32_t* sel_pg = reinterpret_cast<int32_t*>(smem + SM::kPagesOff);
+  // SEL: the page id of list entry lp, -1 unless it is a page of the sequence
+  // above the entry before it, and whole unless it is the last; *cut receives
+  // the slots past the sequence's length in the last one
+  auto resolve = [&](int64_t e, int64_t before, int lp, int sel_n, int64_t sel_seq, int64_t row, int* cut) {
+    const int64_t end = (e + 1) * g.page_size;
+    const bool last = lp == sel_n - 1;
+    int64_t pg = -1;
+    if (e >= 0 && end - g.page_size < sel_seq && e > before && (end <= sel_seq || last))
+      pg = p.page_table ? (int64_t)p.page_table[row * g.max_pages + e] : row * g.max_pages + e;
+    *cut = last && e >= 0 && end > sel_seq && end - g.page_size < sel_seq ? (int)(end - sel_seq) : 0;
+    return pg >= 0 && pg < g.num_pages ? pg : -1;
+  };
+  // ord (SEL): which of the CTA's chunks it is
+  auto issue = [&](const Cursor& c, int stage, int64_t len, int ord = 0) {   // warp-collective
     uint8_t* dst = stg + (size_t)stage * p.stage_bytes;
     // chunk c.c covers logical pages c.c*ppc .. of sequence c.b (32-bit: a
     // sequence holds fewer than 2^31 tokens)
@@ -738,19 +766,19 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
     int64_t pg = -1;
     const int64_t row = p.pf_n > 0 ? p.pf_seq : c.b;   // prefill tiles all read one sequence
     if constexpr (SEL) {
-      // entry lp of the list: a page of the sequence above the entry before
-      // it, and whole unless it is the last
       const int sel_n = (int)len;      // listed pages
-      const int64_t sel_seq = c.nc;    // the sequence's length
       npg = min(ppc, sel_n - (int)c.c * ppc);
-      const int32_t before = __shfl_sync(kFull, entry, (lane + 31) & 31);
-      const int64_t e = entry, end = (e + 1) * g.page_size;
-      const bool last = lp == sel_n - 1;
-      if (lane < npg && e >= 0 && end - g.page_size < sel_seq && e > before && (end <= sel_seq || last))
-        pg = p.page_table ? (int64_t)p.page_table[row * g.max_pages + e] : row * g.max_pages + e;
-      // the last listed page counts up to the sequence's length
-      const int cut = lane < npg && last && e >= 0 && end > sel_seq && end - g.page_size < sel_seq ? (int)(end - sel_seq) : 0;
-      n_tok = npg * g.page_size - __shfl_sync(kFull, cut, npg - 1);
+      int cut = 0;
+      if ((ord + 1) * ppc <= kSelPages) {
+        if (lane < npg) pg = sel_pg[ord * ppc + lane];
+        if ((int)c.c * ppc + npg == sel_n) cut = sel_pg[kSelPages];
+      } else {
+        const int32_t e = entry_of(c.b * g.hkv + c.kvh, c.c);
+        const int32_t before = __shfl_sync(kFull, e, (lane + 31) & 31);
+        if (lane < npg) pg = resolve(e, before, lp, sel_n, c.nc, row, &cut);
+        cut = __shfl_sync(kFull, cut, npg - 1);
+      }
+      n_tok = npg * g.page_size - cut;   // the last listed page counts up to the sequence's length
     } else {
       const int tok0 = (int)c.c * p.chunk_tokens;
       n_tok = min(p.chunk_tokens, (int)len - tok0);
@@ -783,10 +811,27 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
                &full[stage], pol);
   };
   if constexpr (SEL) {
-    // the first stage now, by warp 0, its entries read together with the count
-    // and the length; the others follow once the query is set up, so that the
-    // first chunk of every CTA on the GPU arrives before the second of any
-    if (wid == 0 && nch > 0) issue(Cursor{sel_b, sel_kvh, c0, sel_seq}, 0, sel_n, first_entry);
+    // the pages of the CTA's first chunks: one a thread from the entries read
+    // together with the count and the length, the others later
+    const int ppc = p.pages_per_chunk;
+    auto look_up = [&](int k, int32_t e, int32_t before) {
+      const int i = k / ppc, lp = ((int)c0 + i * p.sel_parts) * ppc + (k - i * ppc);
+      if (k >= kSelPages || k >= nch * ppc || lp >= sel_n) return;
+      if (k >= 32 * kWarps) {
+        const int32_t* list = p.sel_pages + (int64_t)sel_unit * p.sel_row;
+        e = list[lp];
+        before = list[lp - 1];
+      }
+      int cut;
+      sel_pg[k] = (int32_t)resolve(e, before, lp, sel_n, sel_seq, sel_b, &cut);
+      if (lp == sel_n - 1) sel_pg[kSelPages] = cut;
+    };
+    look_up(threadIdx.x, my_entry, my_before);
+    __syncthreads();
+    // the first stage now; the others follow once the query is set up, so that
+    // the first chunk of every CTA on the GPU arrives before the second of any
+    if (wid == 0 && nch > 0) issue(Cursor{sel_b, sel_kvh, c0, sel_seq}, 0, sel_n);
+    for (int k = threadIdx.x + 32 * kWarps; k < kSelPages; k += 32 * kWarps) look_up(k, 0, 0);
   } else {
     Cursor cp = cursor_at(p, c0);  // warp-collective
     if (wid == 0) {
@@ -1543,11 +1588,8 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
     // while the first copies are in flight; the time-out path skips the unit's
     // chunks but not the cluster's merge, so the state is set up in any case
     setup_sel();
-    int32_t entry = first_entry;
-    for (int64_t i = wid; i < nch && i < S; i += kWarps) {   // stages wid, wid + 4, ...
-      if (i > 0) issue(Cursor{sel_b, sel_kvh, c0 + i * p.sel_parts, sel_seq}, (int)i, sel_n, entry);
-      entry = entry_of(sel_unit, c0 + (i + kWarps) * p.sel_parts);
-    }
+    for (int64_t i = wid; i < nch && i < S; i += kWarps)   // stages wid, wid + 4, ...
+      if (i > 0) issue(Cursor{sel_b, sel_kvh, c0 + i * p.sel_parts, sel_seq}, (int)i, sel_n, (int)i);
   }
   const int P = g.page_size;
   int stage = 0;          // i mod S
@@ -1590,8 +1632,7 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
         for (int k = 0; k < S; ++k) cursor_next(p, c);
       const int64_t len = SEL || c.b == b_now ? (int64_t)px.w : seq_len_checked(p, c.b, false);
       fence_proxy_async();
-      if constexpr (SEL) issue(c, prev, len, entry_of((int)pv.x, c.c));
-      else issue(c, prev, len);
+      issue(c, prev, len, SEL ? (int)i - 1 + S : 0);
     }
     const uint32_t st = stg_u32 + (uint32_t)stage * p.stage_bytes;
     const uint4 dv = lds128<0>(st + desc_off);            // unit, b, kvh, n_tok

@@ -318,6 +318,8 @@ ATTN = [
     (dict(lens=(33000, 0, 17), page=16, hkv=1, scale="e4m3zp", d=64, block=32), 3, 2000),
     # long lists of several units: whole clusters, chunks in turn
     (dict(lens=(9000, 8000, 100, 0), page=32, hkv=4, bits=4), 6, 250),
+    # more pages a CTA than it looks up ahead
+    (dict(lens=(70000,), page=16, hkv=1, d=64, block=64, bits=2), 2, 4375),
     # pages larger than a chunk; as large as the copy stages take
     (dict(lens=(700, 300), page=256, hkv=2), 4, 3), (dict(lens=(2500, 1024), page=1024, hkv=1), 4, 2),
 ]
@@ -620,17 +622,20 @@ def _step_buffers(c, G, budget):
     return dict(
         scores=t.empty(*heads, c.maxp, device="cuda"), pages=t.empty(*heads, budget, dtype=t.int32, device="cuda"),
         counts=t.empty(*heads, dtype=t.int32, device="cuda"),
+        q=t.empty(c.B, c.hkv * G, c.d, dtype=t.float16, device="cuda"),
         out=t.empty(c.B, c.hkv * G, c.d, dtype=t.float16, device="cuda"))
 
 
 def _step(c, cache, b, bounds, first, k, v, seq, pos, q, budget):
-    """One decode step of a serving loop over the page operators."""
+    """One decode step of a serving loop over the page operators, with a copy and a kernel of torch's among them."""
     K = c.K
+    b["q"].copy_(q)
     K.kvq3_write(c.rot.handle, c.desc, cache, k, v, seq, pos, c.status)
     K.kvq3_key_bounds(c.desc, cache, first, bounds, c.status)
-    K.kvq3_page_scores(c.rot.handle, c.desc, cache, bounds, q, b["scores"], c.status)
+    K.kvq3_page_scores(c.rot.handle, c.desc, cache, bounds, b["q"], b["scores"], c.status)
+    b["pages"].fill_(-5)
     K.kvq3_page_select(c.desc, cache, b["scores"], budget, 1, 1, b["pages"], b["counts"], c.status)
-    K.kvq3_decode_attn_pages(c.rot.handle, c.desc, cache, q, b["pages"], b["counts"], b["out"], 0.0, c.status)
+    K.kvq3_decode_attn_pages(c.rot.handle, c.desc, cache, b["q"], b["pages"], b["counts"], b["out"], 0.0, c.status)
 
 
 @pytest.mark.parametrize("how", ["eager", "side stream", "graph"])
