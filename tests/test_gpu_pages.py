@@ -146,6 +146,10 @@ def test_key_bounds_bad_lengths_and_pages():
     got, want = _bounds(c)
     assert np.array_equal(got.view(np.uint16), want.view(np.uint16))
     assert c.flags() == c.K.DEV_BITS["bad_len"] | c.K.DEV_BITS["bad_page"]
+    # a negative start
+    c = Pages(lens=(40, 64))
+    got, want = _bounds(c, [-1, 17])
+    assert np.array_equal(got.view(np.uint16), want.view(np.uint16)) and c.flags() == c.K.DEV_BITS["bad_len"]
 
 
 # ------------------------------------------------------------ page scores
@@ -529,13 +533,15 @@ def test_remap_copies_of_many_rows(rows):
     assert _remap(c, np.zeros(rows), np.full(rows, c.lens[0] + 1)) and c.flags() == 0
 
 
-def test_remap_large():
-    # more pages and rows than one pass of the cluster's threads
+@pytest.mark.parametrize("rows,maxp,spare", [(900, 80, 9000), (60, 1100, 3000), (20, 40, 66000), (513, 3, 600), (512, 128, 700)])
+def test_remap_large(rows, maxp, spare):
+    # past what one CTA takes: by rows, by entries, by pages, by one row; and just as much as one CTA takes
     rng = np.random.default_rng(23)
-    lens = rng.integers(0, 1200, 900)
-    c = Pages(d=64, hkv=1, bits=2, scale="e4m3", page=16, lens=lens, maxp=80, spare=9000)
-    assert _remap(c, rng.integers(-1, 900, 900), np.minimum(rng.integers(0, 1280, 900), 700))
-    assert _remap(c, np.arange(900), c.lens + 1)
+    top = 16 * min(maxp, 75)
+    lens = rng.integers(0, top, rows)
+    c = Pages(d=64, hkv=1, bits=2, scale="e4m3", page=16, lens=lens, maxp=maxp, spare=spare)
+    assert _remap(c, rng.integers(-1, rows, rows), np.minimum(rng.integers(0, top, rows), 7 * top // 12))
+    assert _remap(c, np.arange(rows), c.lens + 1) and c.flags() == 0
 
 
 def test_remap_runs_out_of_pages():
@@ -716,6 +722,30 @@ def test_serving_loop(how):
         for w in (0, 1):
             want = O.read_rotated(pool, L, 1, h, w, 0, n0 + 1, table)[1][keep[0, h]]
             assert np.array_equal(O.read_rotated(after, L, 0, h, w, 0, 40, last)[1], want)
+
+
+def test_bad_data_without_a_status_word():
+    # the status word may be left out: bad data is skipped all the same
+    c = Pages(lens=(40, 64, 33), maxp=4)
+    c.lens_t.copy_(c.dev(np.array([40, 65, -3], np.int32)))
+    t, K = c.torch, c.K
+    b = _step_buffers(c, 4, 2)
+    bounds = t.zeros(c.N, c.hkv, 2, c.d, dtype=t.float16, device="cuda")
+    q = c.dev(c.queries(4))
+    K.kvq3_key_bounds(c.desc, c.cache, None, bounds)
+    K.kvq3_page_scores(c.rot.handle, c.desc, c.cache, bounds, q, b["scores"])
+    K.kvq3_page_select(c.desc, c.cache, b["scores"], 2, 0, 1, b["pages"], b["counts"])
+    b["pages"][0, :, 1] = 99
+    K.kvq3_decode_attn_pages(c.rot.handle, c.desc, c.cache, q, b["pages"], b["counts"], b["out"])
+    i32 = lambda x: c.dev(np.array(x, np.int32))   # noqa: E731
+    out, lens = t.empty_like(c.table_t), t.empty_like(c.lens_t)
+    K.kvq3_remap(c.desc, c.cache, i32([0, 7, 1]), i32([41, 5, 3]), out, lens,
+                 t.empty(K.kvq3_remap_workspace_size(c.desc), dtype=t.uint8, device="cuda"))
+    K.kvq3_compact(c.desc, c.cache, i32([0, 0]), i32([0, 1]), t.full((2, c.hkv, 3), -1, dtype=t.int32, device="cuda"), i32([3, 3]))
+    t.cuda.synchronize()
+    assert b["counts"].cpu().tolist() == [[2, 2], [0, 0], [0, 0]] and not b["out"][1:].any()
+    assert lens.cpu().tolist() == [40, 0, 0] and (out[1:] == -1).all()
+    c.pool_now()
 
 
 def test_two_streams():
