@@ -31,6 +31,10 @@
 // random reads 48 + 4 bytes per vector but touches about 104 (whole 32-byte
 // sectors).  16 x 8 heads, 4,096 of 16,384 tokens kept: 31.4 us, 3.5 TB/s of
 // the bytes moved, 5.2 TB/s of sectors (35.6 us with one access at a time).
+//
+// Inputs are read with coherent loads (no __restrict__ on them): a kernel
+// launched as a programmatic dependent is alive while the one before it still
+// writes what it will read.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -298,9 +302,9 @@ __global__ void __launch_bounds__(256)
 // The whole remap of a small table, by every CTA for itself: the first CTA
 // writes the new table and lengths, all copy.
 __global__ void __launch_bounds__(kMapThreads)
-    remap_small_kernel(const __grid_constant__ CacheGeom g, uint8_t* pool, const int32_t* __restrict__ table,
-                       const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ src,
-                       const int32_t* __restrict__ new_lens, int32_t* __restrict__ table_out,
+    remap_small_kernel(const __grid_constant__ CacheGeom g, uint8_t* pool, const int32_t* table,
+                       const int32_t* seq_lens, const int32_t* src,
+                       const int32_t* new_lens, int32_t* __restrict__ table_out,
                        int32_t* __restrict__ lens_out, int32_t* status) {
   __shared__ uint32_t bits[kSmallPages / 32];        // pages held by the new table
   __shared__ uint32_t free_before[kSmallPages / 32]; // free pages before each word
@@ -490,10 +494,10 @@ constexpr int kKeepTile = 128;   // kept tokens per CTA, one per thread
 // access, dividing a token's scales.
 template <typename CV, int CN, typename HV, int HN>
 __global__ void __launch_bounds__(kKeepTile)
-    compact_kernel(const __grid_constant__ CacheGeom g, uint8_t* pool, const int32_t* __restrict__ page_table,
-                   const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ src_seq,
-                   const int32_t* __restrict__ dst_seq, const int32_t* __restrict__ keep,
-                   const int32_t* __restrict__ n_keep, int keep_stride, int tiles, int32_t* status) {
+    compact_kernel(const __grid_constant__ CacheGeom g, uint8_t* pool, const int32_t* page_table,
+                   const int32_t* seq_lens, const int32_t* src_seq,
+                   const int32_t* dst_seq, const int32_t* keep,
+                   const int32_t* n_keep, int keep_stride, int tiles, int32_t* status) {
   __shared__ int64_t from_s[kKeepTile], to_s[kKeepTile];   // K records, -1: skip
   __shared__ int32_t slots_s[kKeepTile];                   // source slot, destination slot << 16
   griddep_wait();

@@ -12,8 +12,9 @@
 // accuracy.  Bound by HBM: 4d bytes per (page, kv head) for 4 d G flops.  Each
 // row's registers are refilled as they are used, so 8 KB a warp stay in
 // flight.  64 sequences of up to 64K tokens, 4 kv heads of 256, 16-token pages
-// (549 MB of bounds): 99 us, 5.5 TB/s, 82 % of the measured copy rate (123 us
-// with a CTA per tile, loading, then computing).  16 sequences of 32K, 8 kv
+// (549 MB of bounds): 94 us, 5.8 TB/s, 86 % of the measured copy rate (123 us
+// with a CTA per tile, loading, then computing; 99 with the bounds through the
+// read-only path).  16 sequences of 32K, 8 kv
 // heads of 128, 128-token pages (17 MB): 5.9 us, latency.
 //
 // Selection.  One CTA per (sequence, kv head): the scores as order-preserving
@@ -24,6 +25,10 @@
 // rows of up to 4,096 pages, 256 of them chosen: 7.3 us (14.4 with three radix
 // passes over keys in shared memory, 11.8 with the keys in registers); 128 rows
 // of 256 pages: 3.5 us.
+//
+// Inputs are read with coherent loads (no __restrict__ on them): a kernel
+// launched as a programmatic dependent is alive while the one before it still
+// writes what it will read.
 #include <math.h>
 
 #include "kvq3_internal.h"
@@ -40,8 +45,8 @@ constexpr int kScoreRounds = 4;
 template <int D, int NT>
 __global__ void __launch_bounds__(32 * kScoreWarps, 2)
     page_scores_kernel(const __grid_constant__ RotParams rp, const __grid_constant__ CacheGeom g,
-                       const int32_t* __restrict__ page_table, const int32_t* __restrict__ seq_lens,
-                       const __half* __restrict__ bounds, const __half* __restrict__ q, int G, int groups, int span,
+                       const int32_t* page_table, const int32_t* seq_lens,
+                       const __half* bounds, const __half* q, int G, int groups, int span,
                        float* __restrict__ scores, int32_t* status, float inv_sqrt_d) {
   constexpr int K = 2 * D;
   constexpr int ROW = K + 32;                // halves per B column in shared memory: 64 bytes of padding, no conflicts
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 2)
   for (int e = 0; e < 2; ++e) {
     const uint4* src = row_of(page[e]);
 #pragma unroll
-    for (int c = 0; c < CH; ++c) a[e][c] = page[e] >= 0 ? __ldg(src + 4 * c) : zero;
+    for (int c = 0; c < CH; ++c) a[e][c] = page[e] >= 0 ? src[4 * c] : zero;
   }
 
   // q1 of the G heads, its negative part against lo and its positive part
@@ -162,8 +167,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 2)
 #pragma unroll
         for (int c = c0; c < c0 + 4 && c < CH; ++c) {
           const uint4 x = a[0][c], y = a[1][c];
-          a[0][c] = there[0] ? __ldg(src[0] + 4 * c) : zero;
-          a[1][c] = there[1] ? __ldg(src[1] + 4 * c) : zero;
+          a[0][c] = there[0] ? src[0][4 * c] : zero;
+          a[1][c] = there[1] ? src[1][4 * c] : zero;
           const uint32_t f0[4] = {x.x, y.x, x.y, y.y}, f1[4] = {x.z, y.z, x.w, y.w};
 #pragma unroll
           for (int t = 0; t < NT; ++t) {
@@ -251,8 +256,8 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 // again from memory each time for longer ones (KPT = 0).
 template <int KPT>
 __global__ void __launch_bounds__(kSelThreads)
-    page_select_kernel(const __grid_constant__ CacheGeom g, const int32_t* __restrict__ seq_lens,
-                       const float* __restrict__ scores, int budget, int sinks, int recent, int32_t* __restrict__ pages,
+    page_select_kernel(const __grid_constant__ CacheGeom g, const int32_t* seq_lens,
+                       const float* scores, int budget, int sinks, int recent, int32_t* __restrict__ pages,
                        int32_t* __restrict__ counts, int32_t* status) {
   __shared__ uint32_t hist[kBins];
   __shared__ uint32_t wsum[kSelWarps];
