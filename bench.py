@@ -85,7 +85,7 @@ def workload_lens(w: I.Workload) -> np.ndarray:
 
 # the source files each profiled kernel is built from (headers included)
 KERNEL_SOURCES = {
-    "decode": ("kvq3_decode.cuh", "kvq3_decode.cu", "kvq3_decode_d*.cu"),
+    "decode": ("kvq3_decode.cuh", "kvq3_decode.cu", "kvq3_decode_d*.cu", "kvq3_stop.h"),
     "write_chunk": ("kvq3_write_chunk.cu",),
     "prefill_tc": ("kvq3_prefill_tc.cu", "kvq3_tc.cuh"),
 }

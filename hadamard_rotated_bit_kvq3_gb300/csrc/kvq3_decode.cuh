@@ -67,6 +67,7 @@
 #include <type_traits>
 
 #include "kvq3_internal.h"
+#include "kvq3_stop.h"
 
 namespace kvq3 {
 
@@ -579,7 +580,7 @@ __host__ __device__ constexpr bool decode_qf_smem(int D, int GPAD) { return D ==
 template <int D, int GPAD, bool SEL = false>
 struct DecodeSmem {
   static constexpr int kFullOff = 0;                              // kMaxStages mbarriers
-  static constexpr int kEmptyOff = kFullOff + 8 * kMaxStages;     // abort flag (+ spare)
+  static constexpr int kEmptyOff = kFullOff + 8 * kMaxStages;     // mark of a wait that ran out (+ spare)
   static constexpr int kMLOff = kEmptyOff + 8 * kMaxStages;       // [kWarps][2][GPAD] floats
   static constexpr int kQOff = (kMLOff + kWarps * 2 * GPAD * 4 + 15) / 16 * 16;  // [GPAD][D]
   static constexpr int kQInvOff = kQOff + GPAD * D * 4;           // [GPAD]
@@ -636,7 +637,7 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
     if (threadIdx.x == 0) {
       uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kFullOff);
       for (int s = 0; s < p.stages; ++s) mbar_init(&bars[s], 1);
-      *reinterpret_cast<volatile uint32_t*>(smem + SM::kEmptyOff) = 0;
+      *reinterpret_cast<volatile uint32_t*>(smem + SM::kEmptyOff) = kNoStop;
       *reinterpret_cast<int32_t*>(smem + SM::kPagesOff + kSelPages * 4) = 0;
       fence_mbar_init();
     }
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
   const int wid = threadIdx.x >> 5;
   const int j = lane & 3, r = lane >> 2;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SM::kFullOff);
-  volatile uint32_t* abort_s = reinterpret_cast<volatile uint32_t*>(smem + SM::kEmptyOff);  // a copy never arrived
+  volatile uint32_t* abort_s = reinterpret_cast<volatile uint32_t*>(smem + SM::kEmptyOff);  // the chunk whose copy never arrived
   float* ml_s = reinterpret_cast<float*>(smem + SM::kMLOff);
   float* qs = reinterpret_cast<float*>(smem + SM::kQOff);
   float* qinv_s = reinterpret_cast<float*>(smem + SM::kQInvOff);
@@ -732,7 +733,7 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
   if constexpr (!SEL) {
     if (threadIdx.x == 0) {
       for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
-      *abort_s = 0;
+      *abort_s = kNoStop;
       fence_mbar_init();
     }
     __syncthreads();
@@ -1596,16 +1597,17 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
   uint32_t parity = 0;    // (i / S) mod 2
   int prev = S - 1;       // (i - 1) mod S
   for (int64_t i = 0; i < nch; ++i) {
-    if (!mbar_wait(&full[stage], parity, p.wait_limit) && lane == 0) *abort_s = 1;
+    if (!mbar_wait(&full[stage], parity, p.wait_limit) && lane == 0) *abort_s = stop_mark(i);
     // One barrier per chunk: the four warps have finished chunk i - 1 and
-    // waited for chunk i.  They decide together whether to go on (every
-    // barrier below is then reached by all of them), and the stage of chunk
-    // i - 1 is free: warp (i - 1) mod 4 refills it with chunk i - 1 + S.
+    // waited for chunk i.  They decide together whether to go on (the mark
+    // names the chunk, see kvq3_stop.h; every barrier below is then reached by
+    // all of them), and the stage of chunk i - 1 is free: warp (i - 1) mod 4
+    // refills it with chunk i - 1 + S.
     // Keeping the warps within one chunk of each other gives every warp the
     // ring's lookahead (a fast warp would otherwise wait on a refill that
     // only the slowest warp can trigger).
     named_barrier(2, 32 * kWarps);
-    if (*abort_s) {
+    if (stops_at(*abort_s, i)) {
       // A copy did not arrive within the bound: flag it, wait for every copy
       // this CTA still has in flight so that no asynchronous write outlives
       // it, and stop.  In flight: chunk i itself (the one that ran out) up to
