@@ -244,6 +244,11 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kBinBits = 11;
 
+// The histogram, read four bins at a time.
+struct __align__(16) Bins {
+  uint32_t n[kBins];
+};
+
 // Order-preserving key: larger score, larger key; NaN lowest, -0 as +0.
 __device__ __forceinline__ uint32_t score_key(float x) {
   if (x != x) return 0u;
@@ -259,7 +264,7 @@ __global__ void __launch_bounds__(kSelThreads)
     page_select_kernel(const __grid_constant__ CacheGeom g, const int32_t* seq_lens,
                        const float* scores, int budget, int sinks, int recent, int32_t* __restrict__ pages,
                        int32_t* __restrict__ counts, int32_t* status) {
-  __shared__ uint32_t hist[kBins];
+  __shared__ Bins hist;
   __shared__ uint32_t wsum[kSelWarps];
   __shared__ uint2 range_s[kSelWarps];   // smallest and largest key of each warp
   __shared__ uint4 found;                // bin, places left in it, its keys
@@ -267,7 +272,7 @@ __global__ void __launch_bounds__(kSelThreads)
   __shared__ unsigned long long cand[32];
   __shared__ uint2 wcount[(KPT > 0 ? KPT : 1) * kSelWarps];   // larger and equal keys of each warp and round
   const int t = threadIdx.x, lane = t & 31, wid = t >> 5;
-  for (int i = t; i < kBins; i += kSelThreads) hist[i] = 0;
+  for (int i = t; i < kBins; i += kSelThreads) hist.n[i] = 0;
   griddep_wait();
   griddep_launch_dependents();
   const int64_t unit = blockIdx.x;
@@ -346,15 +351,16 @@ __global__ void __launch_bounds__(kSelThreads)
   for (int pass = 0;; ++pass) {
     const int shift = max(0, 32 - __clz((int)span) - kBinBits);   // span >> shift < kBins
     if (pass > 0)
-      for (int i = t; i < kBins; i += kSelThreads) hist[i] = 0;
+      for (int i = t; i < kBins; i += kSelThreads) hist.n[i] = 0;
     __syncthreads();
     each([&](uint32_t k, int, int) {
-      if (k - base <= span) atomicAdd(&hist[(k - base) >> shift], 1u);
+      if (k - base <= span) atomicAdd(&hist.n[(k - base) >> shift], 1u);
     });
     __syncthreads();
     // from the top, four bins a thread: the bin that holds the left-th
     constexpr int PER = kBins / kSelThreads;
-    const uint4 h4 = *reinterpret_cast<const uint4*>(&hist[kBins - PER * (t + 1)]);   // bins ascending
+    static_assert(PER == 4 && alignof(Bins) % alignof(uint4) == 0, "a thread's bins are one 16-byte load");
+    const uint4 h4 = *reinterpret_cast<const uint4*>(&hist.n[kBins - PER * (t + 1)]);   // bins ascending
     const uint32_t h[PER] = {h4.w, h4.z, h4.y, h4.x};
     const uint32_t mine = h[0] + h[1] + h[2] + h[3];
     uint32_t incl = mine;
