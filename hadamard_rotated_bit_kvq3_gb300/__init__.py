@@ -335,12 +335,15 @@ def kvq3_dequant_debug(h, desc: CacheDesc, cache: Cache, seq: int, kv_head: int,
 
 # ---- page operators (sparse decode, page management).  These calls take
 # several tensors whose shapes must agree with the cache description, so the
-# binding checks them: a tensor of another type, shape, layout or device is a
-# ValueError before anything is launched.  They are called once or more per
-# decode step and layer, where the kernels take a few microseconds, so the
-# checks read each attribute once and pointers are passed as plain integers
-# (4 to 11 us less a call than through torch.cuda's stream objects).
+# binding checks them: a tensor (the status word's too) of another type, shape,
+# layout or device is a ValueError before
+# anything is launched.  They are called once or more per decode step and
+# layer, where the kernels take a few microseconds, so the checks read each
+# attribute once and pointers are passed as plain integers (4 to 11 us less a
+# call than through torch.cuda's stream objects).
 def _refuse(t, name: str, dtype, shape, where: str):
+    if not isinstance(t, _torch().Tensor):
+        raise ValueError(f"{where}: {name} must be a CUDA tensor of type {dtype}; got {type(t).__name__}")
     raise ValueError(f"{where}: {name} must be a contiguous CUDA tensor on the current device, of type {dtype} and "
                      f"shape {shape}; got {t.dtype} {tuple(t.shape)} on {t.device}"
                      + ("" if t.is_contiguous() else ", not contiguous"))
@@ -373,8 +376,16 @@ def _raw_stream(stream):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _word(dev_status):
-    return None if dev_status is None else dev_status.data_ptr()
+def _word(dev_status, where: str):
+    """Address of the status word: the first element of an int32 tensor."""
+    if dev_status is None:
+        return None
+    t = _torch()
+    if isinstance(dev_status, t.Tensor) and dev_status.dtype is t.int32 and dev_status.numel() > 0:
+        d = dev_status.get_device()
+        if d >= 0 and d == t._C._cuda_getDevice():
+            return dev_status.data_ptr()
+    _refuse(dev_status, "dev_status", t.int32, "of at least one element", where)
 
 
 def kvq3_key_bounds(desc: CacheDesc, cache: Cache, first_pos, bounds, dev_status=None, stream=None) -> None:
@@ -384,7 +395,7 @@ def kvq3_key_bounds(desc: CacheDesc, cache: Cache, first_pos, bounds, dev_status
     t, w = _torch(), "kvq3_key_bounds"
     first = None if first_pos is None else _at(first_pos, "first_pos", t.int32, (desc.batch,), w)
     rows = (max(desc.num_pages, bounds.shape[0]), desc.num_kv_heads, 2, desc.head_dim)
-    _check(lib.kvq3_key_bounds(desc, cache, first, _at(bounds, "bounds", t.float16, rows, w), _word(dev_status),
+    _check(lib.kvq3_key_bounds(desc, cache, first, _at(bounds, "bounds", t.float16, rows, w), _word(dev_status, w),
                                _raw_stream(stream)), w)
 
 
@@ -396,7 +407,7 @@ def kvq3_page_scores(h, desc: CacheDesc, cache: Cache, bounds, q, scores, dev_st
     _check(lib.kvq3_page_scores(
         h, desc, cache, _at(bounds, "bounds", t.float16, (max(desc.num_pages, bounds.shape[0]), hkv, 2, d), w),
         _at(q, "q", t.float16, (b, hq, d), w), hq,
-        _at(scores, "scores", t.float32, (b, hkv, desc.max_pages_per_seq), w), _word(dev_status), _raw_stream(stream)), w)
+        _at(scores, "scores", t.float32, (b, hkv, desc.max_pages_per_seq), w), _word(dev_status, w), _raw_stream(stream)), w)
 
 
 def kvq3_page_select(desc: CacheDesc, cache: Cache, scores, budget: int, sinks: int, recent: int, pages, counts,
@@ -408,7 +419,7 @@ def kvq3_page_select(desc: CacheDesc, cache: Cache, scores, budget: int, sinks: 
     _check(lib.kvq3_page_select(
         desc, cache, _at(scores, "scores", t.float32, (b, hkv, desc.max_pages_per_seq), w), budget, sinks, recent,
         _at(pages, "pages", t.int32, (b, hkv, budget), w), _at(counts, "counts", t.int32, (b, hkv), w),
-        _word(dev_status), _raw_stream(stream)), w)
+        _word(dev_status, w), _raw_stream(stream)), w)
 
 
 def kvq3_decode_attn_pages(h, desc: CacheDesc, cache: Cache, q, pages, counts, out, sm_scale: float = 0.0,
@@ -421,7 +432,7 @@ def kvq3_decode_attn_pages(h, desc: CacheDesc, cache: Cache, q, pages, counts, o
     _check(lib.kvq3_decode_attn_pages(
         h, desc, cache, _at(q, "q", t.float16, rows, w), hq, sm_scale, _at(pages, "pages", t.int32, (b, hkv, n), w),
         _at(counts, "counts", t.int32, (b, hkv), w), n, _at(out, "out", t.float16, rows, w),
-        _word(dev_status), _raw_stream(stream)), w)
+        _word(dev_status, w), _raw_stream(stream)), w)
 
 
 def _workspace(ws, where: str):
@@ -447,7 +458,7 @@ def kvq3_remap(desc: CacheDesc, cache: Cache, src, new_lens, table_out, lens_out
     _check(lib.kvq3_remap(
         desc, cache, _at(src, "src", t.int32, rows, w), _at(new_lens, "new_lens", t.int32, rows, w),
         _at(table_out, "table_out", t.int32, (desc.batch, desc.max_pages_per_seq), w),
-        _at(lens_out, "lens_out", t.int32, rows, w), *_workspace(workspace, w), _word(dev_status),
+        _at(lens_out, "lens_out", t.int32, rows, w), *_workspace(workspace, w), _word(dev_status, w),
         _raw_stream(stream)), w)
 
 
@@ -460,7 +471,7 @@ def kvq3_compact(desc: CacheDesc, cache: Cache, src_seq, dst_seq, keep, n_keep, 
     _check(lib.kvq3_compact(
         desc, cache, _at(src_seq, "src_seq", t.int32, rows, w), _at(dst_seq, "dst_seq", t.int32, rows, w), n,
         _at(keep, "keep", t.int32, (n, desc.num_kv_heads, stride), w), _at(n_keep, "n_keep", t.int32, rows, w), stride,
-        _word(dev_status), _raw_stream(stream)), w)
+        _word(dev_status, w), _raw_stream(stream)), w)
 
 
 class Rotation:
