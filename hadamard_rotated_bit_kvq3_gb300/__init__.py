@@ -336,7 +336,7 @@ def kvq3_dequant_debug(h, desc: CacheDesc, cache: Cache, seq: int, kv_head: int,
 # ---- page operators (sparse decode, page management).  These calls take
 # several tensors whose shapes must agree with the cache description, so the
 # binding checks them: a tensor (the status word's too) of another type, shape,
-# layout or device is a ValueError before
+# layout or device, or something that is no tensor, is a ValueError before
 # anything is launched.  They are called once or more per decode step and
 # layer, where the kernels take a few microseconds, so the checks read each
 # attribute once and pointers are passed as plain integers (4 to 11 us less a
@@ -351,11 +351,16 @@ def _refuse(t, name: str, dtype, shape, where: str):
 
 def _at(t, name: str, dtype, shape, where: str) -> int:
     """Address of a tensor that is as the call needs it."""
-    if t.dtype is dtype and t.shape == shape and t.is_contiguous():
+    if isinstance(t, _torch().Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous():
         d = t.get_device()   # -1: not a CUDA tensor
         if d >= 0 and d == _torch()._C._cuda_getDevice():
             return t.data_ptr()
     _refuse(t, name, dtype, shape, where)
+
+
+def _size(t, dims: int, i: int) -> int:
+    """Extent i of a tensor of `dims` dimensions; -1 for anything else, a shape that _at refuses."""
+    return t.shape[i] if isinstance(t, _torch().Tensor) and t.dim() == dims else -1
 
 
 _torch_module = None
@@ -394,7 +399,7 @@ def kvq3_key_bounds(desc: CacheDesc, cache: Cache, first_pos, bounds, dev_status
     None: 0) on; the others are left as they were."""
     t, w = _torch(), "kvq3_key_bounds"
     first = None if first_pos is None else _at(first_pos, "first_pos", t.int32, (desc.batch,), w)
-    rows = (max(desc.num_pages, bounds.shape[0]), desc.num_kv_heads, 2, desc.head_dim)
+    rows = (max(desc.num_pages, _size(bounds, 4, 0)), desc.num_kv_heads, 2, desc.head_dim)
     _check(lib.kvq3_key_bounds(desc, cache, first, _at(bounds, "bounds", t.float16, rows, w), _word(dev_status, w),
                                _raw_stream(stream)), w)
 
@@ -403,9 +408,9 @@ def kvq3_page_scores(h, desc: CacheDesc, cache: Cache, bounds, q, scores, dev_st
     """scores: fp32 [B][Hkv][max_pages_per_seq] of the queries q, fp16
     [B][Hq][d], against each page's bounds, fp16 [num_pages or more][Hkv][2][d]."""
     t, w = _torch(), "kvq3_page_scores"
-    b, hkv, d, hq = desc.batch, desc.num_kv_heads, desc.head_dim, q.shape[1]
+    b, hkv, d, hq = desc.batch, desc.num_kv_heads, desc.head_dim, _size(q, 3, 1)
     _check(lib.kvq3_page_scores(
-        h, desc, cache, _at(bounds, "bounds", t.float16, (max(desc.num_pages, bounds.shape[0]), hkv, 2, d), w),
+        h, desc, cache, _at(bounds, "bounds", t.float16, (max(desc.num_pages, _size(bounds, 4, 0)), hkv, 2, d), w),
         _at(q, "q", t.float16, (b, hq, d), w), hq,
         _at(scores, "scores", t.float32, (b, hkv, desc.max_pages_per_seq), w), _word(dev_status, w), _raw_stream(stream)), w)
 
@@ -427,7 +432,7 @@ def kvq3_decode_attn_pages(h, desc: CacheDesc, cache: Cache, q, pages, counts, o
     """q, out: fp16 [B][Hq][d]; pages: int32 [B][Hkv][n], strictly ascending;
     counts: int32 [B][Hkv]."""
     t, w = _torch(), "kvq3_decode_attn_pages"
-    b, hkv, hq, n = desc.batch, desc.num_kv_heads, q.shape[1], pages.shape[2]
+    b, hkv, hq, n = desc.batch, desc.num_kv_heads, _size(q, 3, 1), _size(pages, 3, 2)
     rows = (b, hq, desc.head_dim)
     _check(lib.kvq3_decode_attn_pages(
         h, desc, cache, _at(q, "q", t.float16, rows, w), hq, sm_scale, _at(pages, "pages", t.int32, (b, hkv, n), w),
@@ -438,7 +443,7 @@ def kvq3_decode_attn_pages(h, desc: CacheDesc, cache: Cache, q, pages, counts, o
 def _workspace(ws, where: str):
     """Address and bytes of a workspace tensor."""
     t = _torch()
-    n = ws.shape[0] if ws.dim() == 1 else -1
+    n = _size(ws, 1, 0)
     return _at(ws, "workspace", t.uint8, (n,), where), n
 
 
@@ -466,7 +471,7 @@ def kvq3_compact(desc: CacheDesc, cache: Cache, src_seq, dst_seq, keep, n_keep, 
     """src_seq, dst_seq, n_keep: int32 [n]; keep: int32 [n][Hkv][k], positions
     of the source that become positions 0, 1, ... of the destination."""
     t, w = _torch(), "kvq3_compact"
-    n, stride = src_seq.shape[0], keep.shape[-1]
+    n, stride = _size(src_seq, 1, 0), _size(keep, 3, 2)
     rows = (n,)
     _check(lib.kvq3_compact(
         desc, cache, _at(src_seq, "src_seq", t.int32, rows, w), _at(dst_seq, "dst_seq", t.int32, rows, w), n,

@@ -1,5 +1,5 @@
-"""What the page operators' binding refuses before anything is launched: a status word that is no int32 CUDA
-tensor.  No GPU needed: the library's functions are
+"""What the page operators' binding refuses before anything is launched: a status word that is no int32 CUDA tensor, a
+tensor of another number of dimensions, something that is no tensor.  No GPU needed: the library's functions are
 replaced by one that fails the test when it is called."""
 import os
 
@@ -60,3 +60,23 @@ def test_a_status_word_that_is_no_cuda_int32(K, monkeypatch, status):
     for name, call in _calls(K):
         with pytest.raises(ValueError, match="dev_status"):
             call(status)
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("bounds", _z(128, t=torch.float16)), ("bounds", torch.tensor(1.0, dtype=torch.float16)), ("q", _z(3, t=torch.float16)),
+    ("q", _z(3, 8, 128, 1, t=torch.float16)), ("pages", _z(3, 2)), ("keep", _z(2, 2)), ("keep", torch.tensor(3, dtype=torch.int32)),
+    ("ids", torch.tensor(1, dtype=torch.int32)), ("ws", torch.tensor(1, dtype=torch.uint8)),
+    ("bounds", np.zeros((12, 2, 2, 128), np.float16)), ("q", None), ("pages", [0, 1]), ("first", np.zeros(3, np.int32)),
+    ("scores", None), ("counts", 4096), ("src", [0, 1, 2]), ("table", None), ("ws", bytearray(4096)), ("keep", None), ("n_keep", None)])
+def test_other_dimensions_and_no_tensors(K, monkeypatch, name, bad):
+    # device and alignment aside, every tensor but the bad one is as it should be: only that one is refused
+    monkeypatch.setattr(K, "lib", _Library())
+    plain = K._at
+    monkeypatch.setattr(K, "_at", lambda t, *a: plain(t, *a) if t is bad else 4096)
+    found = 0
+    for op, call in _calls(K, **{name: bad}):
+        try:
+            call(_z(0))                  # refused in any case: by its status word where the bad tensor plays no part
+        except ValueError as e:
+            found += "dev_status" not in str(e)
+    assert found
