@@ -188,8 +188,11 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 2)
     for (int t = 0; t < NT; ++t) {
       const float f = qinv[4 * t + j];
       if (4 * t + j < G) {
-        best0 = fmaxf(best0, (sum[t][0] + sum[t][1]) * f);
-        best1 = fmaxf(best1, (sum[t][2] + sum[t][3]) * f);
+        // an infinite bound meets a zero query part (0 times infinity): a sum
+        // that is no number counts as +infinity, so that its page is attended
+        const float s0 = (sum[t][0] + sum[t][1]) * f, s1 = (sum[t][2] + sum[t][3]) * f;
+        best0 = fmaxf(best0, s0 == s0 ? s0 : INFINITY);
+        best1 = fmaxf(best1, s1 == s1 ? s1 : INFINITY);
       }
     }
 #pragma unroll

@@ -476,7 +476,9 @@ kvq3_status kvq3_key_bounds(const kvq3_cache_desc *desc, const kvq3_cache *cache
  * q1 = U q, scores[b][h][i] = max over the Hq/Hkv query heads of kv head h of
  * sum_j max(q1_j lo_j, q1_j hi_j), page i of sequence b.  Up to the fp16
  * rounding of the bounds that is at least every q1 . k_hat of the page (the
- * logits before sm_scale).  Entries of pages at or past seq_lens[b], of a
+ * logits before sm_scale).  A page with an infinite bound (a key past the fp16
+ * range) or one that is no number scores +infinity, so that it is attended
+ * rather than lost.  Entries of pages at or past seq_lens[b], of a
  * sequence with a bad length (KVQ3_DEV_BAD_LEN) and of bad page ids
  * (KVQ3_DEV_BAD_PAGE) are -infinity.
  * q: device fp16 [batch][Hq][d], 16-byte aligned; bounds: device fp16

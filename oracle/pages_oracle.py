@@ -51,7 +51,7 @@ def key_bounds(pool, layout, lens, table, bounds, first_pos=None):
 
 
 def page_scores(bounds, layout, U, q, lens, table):
-    """(scores fp64 [B][Hkv][maxp], -inf where there is no page; tol: an error bound of an fp32 computation).
+    """(scores fp64 [B][Hkv][maxp], -inf where there is no page, +inf where a bound is not finite; tol: an error bound of an fp32 computation).
 
     The bound: q1 by a fast transform in fp32, log2(d) additions, a scaling and up to two quaternion products
     (8 products and sums), each rounding at most 2^-24 of |q|: 2^-24 (log2 d + 10) |q| per element, against
@@ -73,6 +73,9 @@ def page_scores(bounds, layout, U, q, lens, table):
                 continue
             for h in range(hkv):
                 lo, hi = bounds[page, h].astype(np.float64)
+                if not np.isfinite(lo).all() or not np.isfinite(hi).all():
+                    out[b, h, lp] = np.inf      # a key past the fp16 range: attended
+                    continue
                 out[b, h, lp] = np.maximum(q1[b, h] * lo, q1[b, h] * hi).sum(-1).max()
                 m = np.maximum(np.abs(lo), np.abs(hi))
                 tol[b, h, lp] = ((4 * d + 2) * 2.0 ** -23 * (np.abs(q1[b, h]) * m).sum(-1)
