@@ -83,6 +83,32 @@ def page_scores(bounds, layout, U, q, lens, table):
     return out, tol
 
 
+def page_scores_size(bounds, layout, U, q, lens, table):
+    """T fp64 [B][Hkv][maxp]: the largest over the heads of sum_j |q1_j| max(|lo_j|, |hi_j|), 0 where there is no page."""
+    B, hkv, d = len(lens), layout.num_kv_heads, layout.d
+    q1 = np.abs(q.astype(np.float64) @ U.T).reshape(B, hkv, -1, d)
+    out = np.zeros((B, hkv, layout.max_pages_per_seq))
+    for b, n in enumerate(lens):
+        for lp in range(num_pages_of(layout, n)):
+            m = np.abs(bounds[layout.page_id(table, b, lp)].astype(np.float64)).max(1)      # [hkv][d]
+            out[b, :, lp] = np.einsum("hgd,hd->hg", q1[b], m).max(-1)
+    return out
+
+
+# What the root mean square over many pages of a score's error may be, of the root mean square of T (page_scores_size).
+# The worst case of page_scores' tolerance charges every rounding in full and in the same direction, so at d = 128 and
+# 256 it would let a score through whose query lost its low half.  In units of 2^-23, the step of fp32:
+#   0.4  the split: hi + lo leave at most 2^-22 of each query element, of either sign: sqrt(d) of them add up to d
+#        terms, 2 / (0.8 sqrt(d)) at d = 64;
+#   2.3  chains of 8 steps in the tensor core's accumulator, each cutting half a step of the running sum on average and
+#        towards zero; the sum grows to its last value over the chain: (1 + 2 + ... + 8) / 8 / 2;
+#   0.8  the chains' sums added in fp32, and the scaling;
+#   0.5  the rotation in fp32: log2(d) + 10 roundings of 2^-24 of an element, independent over d elements, so that
+#        their sum is at most sqrt(16) 2^-24 / (0.8 sqrt(d)) of T at d = 64.
+# Chains of 32 steps, as d = 256 would have without the sums between, cut 8.3 instead of 2.3.
+SCORE_RMS = 4 * 2.0 ** -23
+
+
 def page_select(scores, layout, lens, budget, sinks, recent):
     """(pages int32 [B][Hkv][budget], counts int32 [B][Hkv]) by a Python sort."""
     B, hkv, _ = scores.shape
