@@ -105,7 +105,6 @@ def page_scores_size(bounds, layout, U, q, lens, table):
 #   0.8  the chains' sums added in fp32, and the scaling;
 #   0.5  the rotation in fp32: log2(d) + 10 roundings of 2^-24 of an element, independent over d elements, so that
 #        their sum is at most sqrt(16) 2^-24 / (0.8 sqrt(d)) of T at d = 64.
-# Chains of 32 steps, as d = 256 would have without the sums between, cut 8.3 instead of 2.3.
 SCORE_RMS = 4 * 2.0 ** -23
 
 

@@ -1,5 +1,5 @@
 """Page scores' root mean square error over many pages against 64 bits: a bar that a lost or misplaced low half of the
-query, or one long chain in the accumulator, does not pass (tests/test_pages_accuracy.py shows that on the CPU)."""
+query does not pass (tests/test_pages_accuracy.py shows that on the CPU)."""
 import numpy as np
 import pytest
 

@@ -1,6 +1,6 @@
 """The bar on the page scores' root mean square error (oracle/pages_oracle.py: SCORE_RMS) on the CPU: the kernel's
 scheme, computed here as it is written down, passes it; the same without the low half of the query, or with that half
-in the wrong place, does not, at any head dimension, nor does one long chain in the accumulator at the largest."""
+in the wrong place, does not, at any head dimension."""
 import numpy as np
 import pytest
 
@@ -68,9 +68,11 @@ def test_the_bar_tells_a_lost_half(d, G):
     assert rms_error(*c, lambda hi, lo: (hi, np.roll(lo, 1))) > PO.SCORE_RMS
 
 
-def test_the_bar_tells_a_long_chain():
+def test_long_chains_cost_more():
+    # why the kernel adds up in fp32 after 8 steps: the cuts of one chain of 32 grow with its running sum (the bar
+    # leaves room for the rest of the scheme and is not what tells them)
     c = case(256, 4)
-    assert rms_error(*c, lambda hi, lo: (hi, lo), 32) > PO.SCORE_RMS
+    assert rms_error(*c, lambda hi, lo: (hi, lo), 32) > 2 * rms_error(*c, lambda hi, lo: (hi, lo), 8)
 
 
 def test_the_size_is_an_upper_bound():
