@@ -330,7 +330,9 @@ __global__ void __launch_bounds__(kThreads)
       const int64_t lp = on ? pfirst[l] + item - (l ? psum[l - 1] : 0) : 0;
       const int64_t page = on ? page_of(g, page_table, b, lp) : -1;
       const bool ok = page >= 0 && KVQ3_CHECK(status, in_range(record_offset(g, page, kvh, 0), g.record_bytes,
-                                                              g.num_pages * g.page_bytes));
+                                                              g.num_pages * g.page_bytes) &&
+                                                         in_range((page * g.hkv + kvh) * 2 * g.d, 2 * g.d,
+                                                                  g.num_pages * g.hkv * 2 * g.d));
       if (on && page < 0 && grp == 0 && s == 0) set_status(status, KVQ3_DEV_BAD_PAGE);
       Accum<NBIT, SCALE> acc;
       acc.init();

@@ -1735,6 +1735,7 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
     // eight lanes of a 16-byte store share a bank.
     constexpr int OROW = D + 16;
     float* part_s = reinterpret_cast<float*>(stg);   // [kWarps][GPAD][OROW]
+    const bool fits = KVQ3_CHECK(p.status, SM::kStageOff + kWarps * GPAD * OROW * (int)sizeof(float) <= (int)p.smem_bytes);
     named_barrier(1, 128);
 #pragma unroll
     for (int tq = 0; tq < NTQ; ++tq) {
@@ -1782,7 +1783,7 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
           float* dst = mine + (PSPLIT ? 4 * tp + j : 8 * tp + 2 * j + c) * OROW + b * BLOCK + r * FV;
 #pragma unroll
           for (int f = 0; f < FV; f += 4)
-            *reinterpret_cast<float4*>(dst + f) = make_float4(v[f], v[f + 1], v[f + 2], v[f + 3]);
+            if (fits) *reinterpret_cast<float4*>(dst + f) = make_float4(v[f], v[f + 1], v[f + 2], v[f + 3]);
         }
       }
     }

@@ -78,6 +78,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 2)
   auto page_at = [&](int64_t lp) {
     const int64_t p = lp < n ? page_of(g, page_table, b, lp) : -1;
     if (lp < n && p < 0 && j == 0) set_status(status, KVQ3_DEV_BAD_PAGE);
+    if (p >= 0 && !KVQ3_CHECK(status, in_range((p * g.hkv + kvh) * K, K, g.num_pages * g.hkv * K))) return (int64_t)-1;
     return p;
   };
   auto row_of = [&](int64_t page) {
