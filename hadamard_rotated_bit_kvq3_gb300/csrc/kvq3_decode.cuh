@@ -572,6 +572,20 @@ struct ChunkDesc {
 // where they would take 32+ registers; elsewhere in registers.
 __host__ __device__ constexpr bool decode_qf_smem(int D, int GPAD) { return D == 256 || GPAD == 16; }
 
+// Whether one of the list's entries [k, n) is a page of a sequence of seq
+// tokens (SEL; a list that is ascending and names pages alone needs no call).
+static __device__ __noinline__ bool page_follows(const int32_t* list, int k, int n, int page_size, int64_t seq) {
+  bool found = false;
+  for (; !found && k < n; k += 8) {
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int64_t x = k + u < n ? list[k + u] : -1;
+      found |= x >= 0 && x * page_size < seq;
+    }
+  }
+  return found;
+}
+
 // SEL: the q1 fragments pass through shared memory in every variant (the warps
 // build them in shares), over the rotated query they are made of (the same
 // size), and the logit seeds come as a part per warp; the page ids of the
@@ -587,7 +601,7 @@ struct DecodeSmem {
   static constexpr int kKofsOff = kQInvOff + GPAD * 4;            // [D/32][GPAD] logit seeds
   static constexpr int kQEnd = (kKofsOff + (SEL ? kWarps : 1) * (D / 32) * GPAD * 4 + 15) / 16 * 16;
   static constexpr int kQfOff = SEL ? kQOff : kQEnd;              // [D/16][GPAD/4][32] uint2
-  static constexpr int kPagesOff = kQEnd;                         // SEL: [kSelPages] page ids, then the cut
+  static constexpr int kPagesOff = kQEnd;                         // SEL: [kSelPages] page ids, the cut, the list's end
   static constexpr int kStageOff =
       ((kQEnd + (SEL ? kSelPages * 4 + 16 : decode_qf_smem(D, GPAD) ? (D / 16) * (GPAD / 4) * 256 : 0)) + 127) / 128 * 128;
 };
@@ -744,16 +758,17 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
   // stages; afterwards the last warp to release a stage refills it
   const uint64_t pol = policy_evict_first();
   int32_t* sel_pg = reinterpret_cast<int32_t*>(smem + SM::kPagesOff);
-  // SEL: the page id of list entry lp, -1 unless it is a page of the sequence
-  // above the entry before it, and whole unless it is the last; *cut receives
-  // the slots past the sequence's length in the last one
-  auto resolve = [&](int64_t e, int64_t before, int lp, int sel_n, int64_t sel_seq, int64_t row, int* cut) {
+  // SEL: the page id of a list entry, -1 unless it is a page of the sequence
+  // above the entry before it and, where it is part-filled, no page of the
+  // sequence follows it (last()); *cut receives the slots past the sequence's
+  // length in the last one
+  auto resolve = [&](int64_t e, int64_t before, int64_t sel_seq, int64_t row, auto last, int* cut) {
     const int64_t end = (e + 1) * g.page_size;
-    const bool last = lp == sel_n - 1;
+    const bool part = e >= 0 && end > sel_seq && end - g.page_size < sel_seq && last();
     int64_t pg = -1;
-    if (e >= 0 && end - g.page_size < sel_seq && e > before && (end <= sel_seq || last))
+    if (e >= 0 && e > before && (end <= sel_seq || part))
       pg = p.page_table ? (int64_t)p.page_table[row * g.max_pages + e] : row * g.max_pages + e;
-    *cut = last && e >= 0 && end > sel_seq && end - g.page_size < sel_seq ? (int)(end - sel_seq) : 0;
+    *cut = part ? (int)(end - sel_seq) : 0;
     return pg >= 0 && pg < g.num_pages ? pg : -1;
   };
   // ord (SEL): which of the CTA's chunks it is
@@ -776,7 +791,7 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
       } else {
         const int32_t e = entry_of(c.b * g.hkv + c.kvh, c.c);
         const int32_t before = __shfl_sync(kFull, e, (lane + 31) & 31);
-        if (lane < npg) pg = resolve(e, before, lp, sel_n, c.nc, row, &cut);
+        if (lane < npg) pg = resolve(e, before, c.nc, row, [&] { return lp == sel_n - 1; }, &cut);
         cut = __shfl_sync(kFull, cut, npg - 1);
       }
       n_tok = npg * g.page_size - cut;   // the last listed page counts up to the sequence's length
@@ -815,20 +830,42 @@ __global__ void __launch_bounds__(128, decode_min_blocks(D, GPAD))
     // the pages of the CTA's first chunks: one a thread from the entries read
     // together with the count and the length, the others later
     const int ppc = p.pages_per_chunk;
+    const int32_t* list = p.sel_pages + (int64_t)sel_unit * p.sel_row;
     auto look_up = [&](int k, int32_t e, int32_t before) {
       const int i = k / ppc, lp = ((int)c0 + i * p.sel_parts) * ppc + (k - i * ppc);
       if (k >= kSelPages || k >= nch * ppc || lp >= sel_n) return;
       if (k >= 32 * kWarps) {
-        const int32_t* list = p.sel_pages + (int64_t)sel_unit * p.sel_row;
         e = list[lp];
         before = list[lp - 1];
       }
       int cut;
-      sel_pg[k] = (int32_t)resolve(e, before, lp, sel_n, sel_seq, sel_b, &cut);
-      if (lp == sel_n - 1) sel_pg[kSelPages] = cut;
+      sel_pg[k] = (int32_t)resolve(
+          e, before, sel_seq, sel_b,
+          [&] { return lp == sel_n - 1 || !page_follows(list, lp + 1, sel_n, g.page_size, sel_seq); }, &cut);
+      if (cut > 0) sel_pg[kSelPages] = cut;
     };
+    // the list ends at its last entry that is a page: what follows is padding,
+    // left out here (one load, under way with those of the page table)
+    int32_t tail = -1;
+    if (wid == kWarps - 1 && lane < sel_n) tail = list[sel_n - 1 - lane];
     look_up(threadIdx.x, my_entry, my_before);
+    if (wid == kWarps - 1) {
+      int end = sel_n;
+      for (;;) {
+        const uint32_t in = __ballot_sync(kFull, tail >= 0 && (int64_t)tail * g.page_size < sel_seq);
+        end = in ? end - __ffs(in) + 1 : max(end - 32, 0);
+        if (in || end == 0) break;
+        tail = lane < end ? list[end - 1 - lane] : -1;
+      }
+      if (lane == 0) sel_pg[kSelPages + 1] = end;
+    }
     __syncthreads();
+    if (sel_pg[kSelPages + 1] != sel_n) {
+      sel_n = sel_pg[kSelPages + 1];
+      if (threadIdx.x == 0 && sel_part == 0) set_status(p.status, KVQ3_DEV_BAD_PAGE);
+      const int nc = (sel_n + ppc - 1) / ppc;
+      nch = nc > sel_part ? (nc - sel_part + p.sel_parts - 1) / p.sel_parts : 0;
+    }
     // the first stage now; the others follow once the query is set up, so that
     // the first chunk of every CTA on the GPU arrives before the second of any
     if (wid == 0 && nch > 0) issue(Cursor{sel_b, sel_kvh, c0, sel_seq}, 0, sel_n);

@@ -131,7 +131,8 @@ def page_select(scores, layout, lens, budget, sinks, recent):
 
 
 def decode_pages(pool, layout, U, q, lens, table, pages, counts, sm_scale=0.0):
-    """fp64 [B][Hq][d]: attention of each head over the listed pages (strictly ascending; others left out)."""
+    """fp64 [B][Hq][d]: attention of each head over the listed pages (strictly ascending; others left out, and a
+    part-filled page that another page of the sequence follows)."""
     B, hq, d = q.shape
     hkv, P = layout.num_kv_heads, layout.page_size
     G = hq // hkv
@@ -151,7 +152,7 @@ def decode_pages(pool, layout, U, q, lens, table, pages, counts, sm_scale=0.0):
                 lp = int(pages[b, h, i])
                 if lp < 0 or lp * P >= n or (i > 0 and lp <= int(pages[b, h, i - 1])):
                     continue
-                if (lp + 1) * P > n and i != c - 1:
+                if (lp + 1) * P > n and any(0 <= int(e) and int(e) * P < n for e in pages[b, h, i + 1:c]):
                     continue
                 page = layout.page_id(table, b, lp)
                 if not 0 <= page < layout.num_pages:
