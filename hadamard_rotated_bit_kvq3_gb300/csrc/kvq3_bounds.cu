@@ -23,7 +23,10 @@
 // 16 sequences of 32K tokens (8 kv heads of 128, 3-bit codes, 128-token pages):
 // 87 us, 2.7 TB/s of 235 MB.  Runs of consecutive tokens per lane (constant
 // address steps) took 95 us (one 48-byte piece per memory wavefront), window
-// tables with 5 kinds of field position instead of 8 84 to 88.
+// tables with 5 kinds of field position instead of 8 84 to 88.  The other
+// formats on the same tokens: 83 us at 2 bits, 91 at 4, 87 with E4M3 scales, 95
+// with zero points, 146 with fp32 scales (products in fp32, rounded at the
+// end); 50 us at d = 64 and 169 at d = 256.
 //
 // Inputs are read with coherent loads (no __restrict__ on them): a kernel
 // launched as a programmatic dependent is alive while the one before it still

@@ -310,12 +310,21 @@ namespace {
 // to 1.3 us): a wave of CTAs pays about 6.5 to start and to merge, and an SM is
 // busy with about 2.4 chunks in flight where it holds 4 CTAs, with as many as
 // it holds where registers allow fewer; clusters spread over the SMs to within
-// about 5 %.  Measured (us): 128 units of 16 chunks at 4 CTAs an SM: 1, 2, 3,
+// about 5 %.  The constants are a fit to the first three formats below, not a
+// mechanism; the others were measured after it.  Measured (us): 128 units of 16 chunks at 4 CTAs an SM: 1, 2, 3,
 // 4, 8 CTAs a unit 43.4, 27.5, 32.9, 25.6, 30.2; 64 units of 64 chunks at 3 an
 // SM (G = 8): 4, 5, 6, 8 CTAs 67.8, 58.9, 51.0, 69.0; 256 units of 16 chunks at
 // 3 an SM (d = 256): 1, 2, 3, 4 CTAs 66.1, 65.8, 60.0, 64.3; 1,024 units of 16
 // chunks: 1, 2, 4 CTAs 131, 136, 150; 8 units of 16 chunks: 2, 4, 8 CTAs 21.7,
-// 13.5, 9.2.  (The dense kernel's even split over all CTAs with a second
+// 13.5, 9.2.  Over 1, 2, 3, 4, 6, 8, 12 and 16 CTAs a unit the rule takes the
+// fastest (to 1 %) for d = 64 at G = 4, 8 and 16 (128 units of 4,096 tokens:
+// 16.7 of 16.7 to 36.9, 20.8 of 20.8 to 64.1, 29.3 of 29.3 to 109; 8 units 8.4,
+// 1,024 units 47.4 and 114), d = 128 at G = 16 (128 units 42.6 of 42.6 to 153,
+// 64 units of 16,384 72.8, 512 units of 2,048 85.4) and d = 256 at G = 8 and 16
+// (256 units of 2,048: 55.7, 145; 4 units of 16,384: 52.1).  It misses at 8
+// units of 16,384, d = 128, G = 16 (29.2, best 26.9), 32 units of 4,096, d =
+// 128, G = 8 (17.7, best 16.5) and 32 of 2,048, d = 256, G = 8 (24.8, best
+// 21.2).  (The dense kernel's even split over all CTAs with a second
 // merging kernel took 39.6, 65.3, 83.8, 169 and 18.7.)
 int pages_parts(const DecodePlan& plan, int64_t units, int32_t row) {
   const int sms = std::max(1, sm_count());

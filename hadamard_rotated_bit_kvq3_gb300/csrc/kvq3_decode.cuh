@@ -56,10 +56,11 @@
 // heads, G = 4, d = 128, 4,096 tokens each: 39.6 us with the flattened list and
 // second kernel, 27.8 as clusters, 24.5 now (2.2 TB/s); 8 x 8, G = 8, E4M3
 // scales, 16,384 tokens: 65 to 50.4 us (2.1 TB/s); 64 x 4, d = 256, 16-token
-// pages, 2,048 tokens: 84 to 59 us (1.9 TB/s).  What is left above the loop's
-// own issue rate (1.04 us a 256-token chunk and SM; 1.14 with the look-ups in
-// the refills): about 7 us to start and merge, and SMs that hold 4 CTAs while
-// others hold 3.
+// pages, 2,048 tokens: 84 to 59 us (1.9 TB/s).  What is left: the loop's own
+// pace (1.04 us a 256-token chunk and SM; 1.14 with the look-ups in the
+// refills), which at 12 to 16 warps an SM is latency, with issue slots 39 to 49
+// % busy, the tensor pipe 11 to 20 % and the chunk's barrier the first stall;
+// about 7 us to start and merge; and SMs that hold 4 CTAs while others hold 3.
 #pragma once
 
 #include <float.h>
@@ -2175,7 +2176,13 @@ KVQ3_DECODE_DECL1(64, e4m3zp, 3) KVQ3_DECODE_DECL1(128, e4m3zp, 3) KVQ3_DECODE_D
 // P' split into hi + lo halves for fp32 value scales (p times an fp32 scale is
 // not an fp16 value) and for up to 4 heads per kv head, where the split
 // columns fit the same 8-column PV tile (no extra MMAs) and remove the fp16
-// rounding of P' from the error.
+// rounding of P' from the error.  With more heads and fp16 or E4M3 scales P'
+// is rounded to fp16 once: 1.4e-4 of the output over 16,384 tokens (2-norm,
+// against the fp32 form; 0.8e-4 with the split, the outputs' own fp16 rounding
+// included in both), where the attention over selected pages rounds its
+// output to fp16 anyway (2.1e-4 against 64 bits, 2.07e-4 with the split).  The
+// split at 8 heads doubles the PV MMAs: 49.9 to 59.8 us for 8 x 8 units of
+// 16,384 tokens, 31.1 to 36.8 for 16 x 8 of 4,096, 55.7 to 63.9 at d = 256.
 #define KVQ3_DECODE_PICK(D, BLK, SC, NB, FN, ...)                                             \
   {                                                                                           \
     constexpr bool SPLIT = (SC) == KVQ3_SCALE_F32 || (SC) == KVQ3_SCALE_E4M3_ZP;              \

@@ -21,7 +21,11 @@
 // copies, the only bulk traffic, are a second kernel's, its programmatic
 // dependent.  Only the slots in use are copied.  16 sequences that grow by a
 // token: 5.0 us; 64 sequences in beams of 8, a third of them with a page to
-// copy (2.3 MB): 8.4 us (13.4 and 18.1 as a cluster with a copy kernel).
+// copy (2.3 MB): 8.4 us (13.4 and 18.1 as a cluster with a copy kernel).  Where
+// the two meet: 16 rows of up to 4,095 pages 38.2 us in the one launch, 512 rows
+// of up to 64 pages 27.5; 600 rows of up to 64 pages 23.8 as a cluster.  64 rows
+// of up to 4,096 pages: 67 us, six cluster barriers and eight SMs that walk 2 MB
+// of table.
 //
 // Compaction is a gather of packed vectors (codes and scales as stored); one
 // CTA takes a run of kept tokens of a (sequence, kv head), resolves each
@@ -48,7 +52,8 @@ namespace {
 
 constexpr int kMapThreads = 1024;
 constexpr int kMapCluster = 8;      // CTAs of the remap cluster (the portable maximum)
-// What one CTA takes: a cluster barrier costs over a microsecond with the
+// The tables that remap_small_kernel takes, whose every CTA does the whole
+// bookkeeping for itself: a cluster barrier costs over a microsecond with the
 // workspace's writes in flight, a block barrier almost nothing, but one SM
 // moves only about 100 GB/s of table.
 constexpr int kSmallRows = 512;

@@ -14,8 +14,10 @@
 // flight.  64 sequences of up to 64K tokens, 4 kv heads of 256, 16-token pages
 // (549 MB of bounds): 94 us, 5.8 TB/s, 86 % of the measured copy rate (123 us
 // with a CTA per tile, loading, then computing; 99 with the bounds through the
-// read-only path).  16 sequences of 32K, 8 kv
-// heads of 128, 128-token pages (17 MB): 5.9 us, latency.
+// read-only path).  With 8 and 16 heads per kv
+// head 97 and 113 us; at d = 128 and 64 with 8 heads 52 and 40 us for half and
+// a quarter of the bytes (78 and 52 % of the copy rate).  16 sequences of 32K, 8
+// kv heads of 128, 128-token pages (17 MB): 5.9 us, latency.
 //
 // Selection.  One CTA per (sequence, kv head): the scores as order-preserving
 // 32-bit keys (in registers up to 8,192 pages), a histogram search for the
@@ -24,7 +26,8 @@
 // latency, a few block barriers of a row of a few thousand keys; no sort.  256
 // rows of up to 4,096 pages, 256 of them chosen: 7.3 us (14.4 with three radix
 // passes over keys in shared memory, 11.8 with the keys in registers); 128 rows
-// of 256 pages: 3.5 us.
+// of 256 pages: 3.5 us.  Rows of more than 8,192 pages read their scores again
+// in every pass: 25.8 us for 16,384 pages, 112 for 65,536.
 //
 // Inputs are read with coherent loads (no __restrict__ on them): a kernel
 // launched as a programmatic dependent is alive while the one before it still
@@ -542,6 +545,12 @@ kvq3_status kvq3_page_select(const kvq3_cache_desc* desc, const kvq3_cache* cach
     return cuda_status(cudaLaunchKernelEx(&cfg, kernel, g, cache->seq_lens, scores, budget, sinks, recent, pages, counts,
                                           dev_status));
   };
+  // Measured for 128 rows (us): a kernel with more rounds than the row needs
+  // pays 0.1 to 0.2 a round (512 pages: 1, 2, 3, 4, 8 rounds 3.5, 3.7, 3.9,
+  // 4.0, 4.8), so that 2 or 4 rounds of their own would gain 0.1 and 0.7 at
+  // most (2,048 pages: 4, 6, 8 rounds 4.4, 4.7, 5.0), 12 another 0.9 (6,144
+  // pages: 6.4, and 7.2 with 16); reading again costs 6.7 for 2,048 pages, 9.5
+  // for 4,096, 15.0 for 8,192 (7.6 with 16 rounds).
   const int64_t most = (int64_t)g.max_pages - sinks - recent;
   if (most <= kSelThreads) return run(page_select_kernel<1>);
   if (most <= 3 * kSelThreads) return run(page_select_kernel<3>);
