@@ -58,7 +58,7 @@
 // scales, 16,384 tokens: 65 to 50.4 us (2.1 TB/s); 64 x 4, d = 256, 16-token
 // pages, 2,048 tokens: 84 to 59 us (1.9 TB/s).  What is left: the loop's own
 // pace (1.04 us a 256-token chunk and SM; 1.14 with the look-ups in the
-// refills), which at 12 to 16 warps an SM is latency, with issue slots 39 to 49
+// refills), which at 12 to 16 warps an SM is latency, with issue slots 40 to 51
 // % busy, the tensor pipe 11 to 20 % and the chunk's barrier the first stall;
 // about 7 us to start and merge; and SMs that hold 4 CTAs while others hold 3.
 #pragma once

@@ -25,7 +25,7 @@ def test_page_operators_through_the_checked_build():
     lib = _checked_library()
     env = dict(os.environ, KVQ3_LIBRARY=lib)
     files = [os.path.join(ROOT, "tests", f) for f in ("test_gpu_pages.py", "test_gpu_pages_range.py",
-                                                      "test_gpu_pages_accuracy.py", "test_gpu_stop.py")]
+                                                      "test_gpu_pages_accuracy.py", "test_gpu_pages_lists.py", "test_gpu_stop.py")]
     cmd = [sys.executable, "-m", "pytest", "-q", "-x", "-m", "gpu", "-p", "no:cacheprovider", *files]
     p = subprocess.run(cmd, cwd=ROOT, env=env, capture_output=True, text=True, timeout=1800)
     print(p.stdout[-2000:])
