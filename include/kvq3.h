@@ -510,8 +510,8 @@ kvq3_status kvq3_page_select(const kvq3_cache_desc *desc, const kvq3_cache *cach
  * A list entry that is not a page of the sequence or not above the entry
  * before it is left out (KVQ3_DEV_BAD_PAGE), and so is the sequence's
  * part-filled last page where another of its pages follows in the list (in an
- * ascending list nothing but entries that are no pages can); a bad count or length gives zeros
- * (KVQ3_DEV_BAD_LEN), and so does an empty list.
+ * ascending list nothing but entries that are no pages can); a bad count or
+ * length gives zeros (KVQ3_DEV_BAD_LEN), and so does an empty list.
  * q: device fp16 [batch][Hq][d]; out: device fp16 [batch][Hq][d], what the
  * projection after it reads (one rounding of the fp32 result, 2^-11 relative,
  * below the error bar of the attention); both 16-byte aligned.  No workspace:
